@@ -1,0 +1,692 @@
+// k_paged.cu -- attention of one new token per sequence over a paged key-value cache,
+// split over the cache's length and joined, sm_100a.
+//
+//   o[b,h] = sum_j softmax_j(scale q[b,h] . k_j) v_j,  j in [0, len_b), k_j and v_j in
+//   page table[b][j / page_size] at row j % page_size of key/value head h / (Hq / Hkv).
+//
+// One new token makes 4 d flops per query head and cached byte pair: far below what the
+// tensor cores need to be busy, so the kernel is bound by HBM and everything serves the
+// loads.  The keys and values of every (sequence, key/value head, 16 query heads of the
+// group) are a row of blocks of 64 positions; the blocks of all rows form one list, cut
+// into equal contiguous shares, one per CTA (two CTAs per SM), so ragged lengths, one
+// long sequence and many short ones all load the SMs evenly.  A producer warp fetches the
+// page ids one block ahead and issues one TMA box per run of rows inside a page (at most
+// eight per block, each lane its own) into a ring of stages; four warps take 16 positions
+// of the block each, with their own running maximum, sum and output (one pass, online
+// softmax), and are joined in shared memory where the share leaves a row of blocks.  A row
+// of blocks that lies in one share is finished there; the pieces of the others go to the
+// workspace and a second launch joins them by the log-sum-exp rule.
+//
+// The products run on the warp-level matrix instruction with the query heads as its 16
+// rows: the operands arrive by ldmatrix straight from the swizzled tile and the scores
+// stay in registers as the next product's operand; a 128-row tcgen05 tile would be at
+// most one eighth full and adds a round trip through tensor memory for each block.
+// 8-bit pages: keys and values become fp16 exactly (every e4m3 is one).  A query row is
+// scaled to [-1, 1] by a power of two so that it is fp16 as well (an element below 2^-14 of
+// the row's largest loses bits that the fp32 sum would not keep either); a key's scale
+// multiplies its score and a value's scale its probability, in fp32.
+#include <cuda.h>
+
+#include <mutex>
+
+#include "seq_pages.cuh"
+#include "tc_ptx.cuh"
+#include "tmap.cuh"
+
+namespace stree {
+
+stree_status check_cache(const void *k_pages, const void *v_pages, const void *k_scales, const void *v_scales,
+                         const int32_t *table, int batch, int heads_kv, int head_dim, int n_pages, int page_size,
+                         int max_pages, stree_dtype cache);
+
+namespace {
+
+constexpr int kD = kCacheDim;
+constexpr int kBlk = 64;                       // positions per block
+constexpr int kComputeWarps = 4;               // 16 positions each
+constexpr int kThreads = (kComputeWarps + 1) * 32;
+constexpr int kHeadRows = 16;                  // query heads of a matrix instruction
+constexpr int kMaxStages = 8;
+constexpr int kSmemPerCta = 113 * 1024;        // two CTAs per SM
+constexpr int kCombineThreads = 128;
+
+struct PagedArgs {
+    const __nv_bfloat16 *q;
+    const uint8_t *k_scales, *v_scales;
+    const int32_t *table, *lens;
+    __nv_bfloat16 *o;
+    float *part_o;                             // [share][2][rows][128]
+    float2 *part_ml;                           // [share][2][rows]: (reference, sum); sum < 0: bad page
+    int32_t *err;
+    int batch, heads_q, heads_kv, group, row_tiles, rows;   // rows: min(group, 16)
+    int n_pages, page_size, max_pages, box_rows, shares, stages;
+    float scale_log2;
+};
+
+__device__ __forceinline__ int blocks_of(const PagedArgs &a, int b)
+{
+    const int n = min(max(__ldg(a.lens + b), 0), a.max_pages * a.page_size);
+    return (n + kBlk - 1) / kBlk;
+}
+
+__device__ __forceinline__ long long share_begin(long long total, int c, int shares) { return total * c / shares; }
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+template <bool kHalf>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    if (kHalf)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// Two e4m3 -> two bf16, exactly.
+__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t w)
+{
+    const uint32_t h = e4m3x2_to_f16x2(w);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+    return pack_bf16(f.x, f.y);
+}
+
+struct Stage {                                 // offsets inside a stage of the ring
+    uint32_t k, v, ks, vs, bytes;
+};
+
+template <bool kE4m3>
+__host__ __device__ constexpr Stage stage_layout()
+{
+    // 8-bit pages: [64][128 B] tiles and 64 scale bytes each; bf16: two 64-column halves.
+    return kE4m3 ? Stage{0, 8192, 16384, 16384 + 64, 16384 + 1024} : Stage{0, 16384, 0, 0, 32768};
+}
+
+template <bool kE4m3>
+__global__ void __launch_bounds__(kThreads, 2)
+paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                       const PagedArgs a)
+{
+    constexpr Stage L = stage_layout<kE4m3>();
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    __shared__ uint64_t bars[2 * kMaxStages];
+    __shared__ int tmp[33], found[2];
+    __shared__ volatile int aborted, bad[kMaxStages];
+    __shared__ float2 ml_s[kComputeWarps][kHeadRows];
+    uint8_t *smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
+    float *joined = reinterpret_cast<float *>(smem + a.stages * L.bytes);   // [4][rows][128]
+    auto full = [&](int s) { return ptx::smem_u32(&bars[s]); };
+    auto empty = [&](int s) { return ptx::smem_u32(&bars[kMaxStages + s]); };
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    pdl_start();
+    if (blockIdx.x == a.shares) {              // the error word
+        PageCheck c{};
+        c.count = a.lens;
+        c.table = a.table;
+        c.batch = a.batch;
+        c.n_pages = a.n_pages;
+        c.page_size = a.page_size;
+        c.max_pages = a.max_pages;
+        c.clamp = a.max_pages * a.page_size;
+        check_pages(c, a.err);
+        return;
+    }
+    // Rows of sequences with no position are zero.
+    for (int b = blockIdx.x; b < a.batch; b += a.shares)
+        if (blocks_of(a, b) == 0)
+            for (int e = tid; e < a.heads_q * kD / 8; e += kThreads)
+                reinterpret_cast<uint4 *>(a.o + (size_t)b * a.heads_q * kD)[e] = make_uint4(0u, 0u, 0u, 0u);
+    // This CTA's share of the list.
+    const int per_seq = a.heads_kv * a.row_tiles;
+    int n_all = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
+        int t;
+        block_scan(b0 + tid < a.batch ? blocks_of(a, b0 + tid) : 0, tmp, &t);
+        n_all += t;
+    }
+    const long long total = (long long)n_all * per_seq;
+    const int shares = (int)min((long long)a.shares, total);   // no share is empty
+    if ((int)blockIdx.x >= shares) return;
+    const long long begin = share_begin(total, blockIdx.x, shares), end = share_begin(total, blockIdx.x + 1, shares);
+    // The list is ordered by sequence, then by (key/value head, row tile), then by block.
+    block_find(a.batch, (int)(begin / per_seq), [&](int b) { return blocks_of(a, b); }, tmp, found);
+    const int b_first = found[0];
+    const long long seq_at = (long long)found[1] * per_seq;
+
+    if (tid == 0) {
+        for (int s = 0; s < a.stages; ++s) {
+            ptx::mbar_init(full(s), kE4m3 ? 1 + 16 : 1);
+            ptx::mbar_init(empty(s), kComputeWarps);
+        }
+        ptx::fence_mbar_init();
+        aborted = 0;
+    }
+    __syncthreads();
+
+    auto wait = [&](uint32_t bar, uint32_t parity, int where) -> bool {
+        if (aborted) return false;
+        if (ptx::mbar_wait(bar, parity)) return true;
+        if (a.err) latch_error(a.err, STREE_ERR_TIMEOUT, b_first, where, (int)parity);
+        aborted = 1;
+        return false;
+    };
+    // Where the share begins: its sequence, row of blocks (item) and block.
+    int b = b_first, nb = blocks_of(a, b);
+    long long left = end - begin;
+    int item = (int)((begin - seq_at) / nb), blk = (int)((begin - seq_at) % nb);
+    auto advance = [&] {                       // to the next block of the list
+        if (++blk < nb) return;
+        blk = 0;
+        if (++item < per_seq) return;
+        item = 0;
+        do ++b;
+        while (b < a.batch && (nb = blocks_of(a, b)) == 0);
+    };
+
+    if (warp == kComputeWarps) {
+        // ------------------------------------------------------------ producer
+        const int boxes = kBlk / a.box_rows;
+        const uint32_t box_bytes = (uint32_t)a.box_rows * 128u;
+        if (lane == 0) {
+            ptx::prefetch_tensormap(&tm_k);
+            ptx::prefetch_tensormap(&tm_v);
+        }
+        // Lane i < 8 looks up the page of positions 8 i .. 8 i + 7 (an eighth lies in one page).
+        auto lookup = [&](int bb, int bl) -> int {
+            const int pos = bl * kBlk + (lane & 7) * 8;
+            const int n = min(max(__ldg(a.lens + bb), 0), a.max_pages * a.page_size);
+            if (pos >= n) return -2;           // nothing there
+            const int id = __ldg(a.table + (size_t)bb * a.max_pages + pos / a.page_size);
+            return id >= 0 && id < a.n_pages ? id : -1;
+        };
+        int id = lookup(b, blk);
+        uint64_t issued = 0;
+        for (; left > 0; --left, ++issued) {
+            const int s = (int)(issued % a.stages);
+            const int cb = b, citem = item, cblk = blk, cid = id;
+            if (left > 1) {
+                advance();
+                id = lookup(b, blk);
+            }
+            bool ok = true;
+            if (issued >= (uint64_t)a.stages) {
+                if (lane == 0) ok = wait(empty(s), (uint32_t)((issued / a.stages - 1) & 1), 1);
+                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+            }
+            if (!ok) break;
+            const int hkv = citem / a.row_tiles;
+            const int eighth = lane * (a.box_rows / 8);   // of the box that this lane issues
+            const int box_id = __shfl_sync(0xffffffffu, cid, eighth & 7);
+            const bool mine = lane < boxes && box_id >= 0;
+            const uint32_t n_boxes = __popc(__ballot_sync(0xffffffffu, mine));
+            const bool any_bad = __any_sync(0xffffffffu, cid == -1);
+            const uint32_t base = ptx::smem_u32(smem + s * L.bytes);
+            if (lane == 0) {
+                bad[s] = any_bad;
+                ptx::mbar_expect_tx(full(s), n_boxes * box_bytes * (kE4m3 ? 2u : 4u));
+            }
+            __syncwarp();
+            if (mine) {
+                const int pos = cblk * kBlk + lane * a.box_rows;
+                const int row = (box_id * a.heads_kv + hkv) * a.page_size + pos % a.page_size;
+                const uint32_t at = base + (uint32_t)lane * box_bytes;
+                ptx::tma_load_2d(at + L.k, &tm_k, 0, row, full(s));
+                ptx::tma_load_2d(at + L.v, &tm_v, 0, row, full(s));
+                if (!kE4m3) {
+                    ptx::tma_load_2d(at + L.k + 8192, &tm_k, 64, row, full(s));
+                    ptx::tma_load_2d(at + L.v + 8192, &tm_v, 64, row, full(s));
+                }
+            }
+            if (kE4m3 && lane < 16) {
+                // Lanes 0-7 the eighths of the key scales, 8-15 of the value scales.
+                if (cid >= 0) {
+                    const size_t at = ((size_t)cid * a.heads_kv + hkv) * a.page_size + (cblk * kBlk + (lane & 7) * 8) % a.page_size;
+                    ptx::cp_async8(base + (lane < 8 ? L.ks : L.vs) + (lane & 7) * 8, (lane < 8 ? a.k_scales : a.v_scales) + at);
+                }
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full(s)) : "memory");
+            }
+        }
+        // Nothing may still be landing in shared memory when the CTA ends.
+        if (aborted) {
+            if (kE4m3) ptx::cp_async_wait_all();
+            if (lane == 0)
+                for (uint64_t i = issued > (uint64_t)a.stages ? issued - a.stages : 0; i < issued; ++i)
+                    ptx::mbar_wait(full((int)(i % a.stages)), (uint32_t)((i / a.stages) & 1));
+        }
+        return;
+    }
+
+    // ---------------------------------------------------------------- compute
+    const int t4 = lane & 3, r4 = lane >> 2;
+    uint64_t taken = 0;
+    bool run = true;
+    int piece = 0;                             // 0: the share's first row of blocks, 1: a later one
+    while (left > 0 && run) {
+        const int hkv = item / a.row_tiles, rt = item % a.row_tiles;
+        const int head0 = hkv * a.group + rt * kHeadRows;
+        const int rows = min(kHeadRows, a.group - rt * kHeadRows);
+        const int cb = b, blk0 = blk, cnb = nb;
+        const int n = min(max(__ldg(a.lens + cb), 0), a.max_pages * a.page_size);
+        const bool whole = blk0 == 0 && left >= cnb;
+        // Q as the matrix instruction's A operand; rows past the group are zero.  With 8-bit
+        // pages the columns are permuted as the unpacked key bytes lie: k index 2 t, 2 t + 1
+        // of a step is column 4 t, 4 t + 1, and 2 t + 8, 2 t + 9 is 4 t + 2, 4 t + 3.
+        uint32_t qf[8][4];
+        float qs[2] = {a.scale_log2, a.scale_log2};
+        {
+            const __nv_bfloat16 *qp = a.q + ((size_t)cb * a.heads_q + head0) * kD;
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = r4 + (i & 1) * 8;
+                    const int col = kE4m3 ? kk * 16 + t4 * 4 + (i >> 1) * 2 : kk * 16 + t4 * 2 + (i >> 1) * 8;
+                    qf[kk][i] = r < rows ? __ldg(reinterpret_cast<const uint32_t *>(qp + (size_t)r * kD + col)) : 0u;
+                }
+            if (kE4m3) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk) top = max(top, max(finite_top2(qf[kk][i]), finite_top2(qf[kk][i + 2])));
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    // The row's largest magnitude lies in [2^(e-127), 2^(e-126)).
+                    const uint32_t e = min(max(top >> 7, 2u), 252u);
+                    const float inv = power_of_two(253u - e);
+                    qs[i] *= power_of_two(e + 1u);
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+#pragma unroll
+                        for (int j = i; j < 4; j += 2) {
+                            const uint32_t w = qf[kk][j];
+                            const __half2 h = __floats2half2_rn(__uint_as_float(w << 16) * inv,
+                                                                __uint_as_float(w & 0xffff0000u) * inv);
+                            qf[kk][j] = *reinterpret_cast<const uint32_t *>(&h);
+                        }
+                }
+            }
+        }
+        float acc[16][4];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        int any_bad = 0;
+        while (true) {
+            const int s = (int)(taken % a.stages);
+            if (lane == 0) run = wait(full(s), (uint32_t)((taken / a.stages) & 1), 10);
+            run = __shfl_sync(0xffffffffu, run ? 1 : 0, 0) != 0;
+            if (!run) break;
+            any_bad |= bad[s];
+            const uint32_t base = ptx::smem_u32(smem + s * L.bytes);
+            const int key0 = warp * 16, valid = n - (blk * kBlk + key0);   // positions of this warp that exist
+            if (valid > 0) {
+                float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+                if (kE4m3) {
+                    // Matrices: keys 0-7 and 8-15 of a 16-byte chunk, then of the next chunk.
+                    const int row = key0 + (lane & 15);
+#pragma unroll
+                    for (int kk = 0; kk < 8; kk += 2) {
+                        uint32_t r[4];
+                        ldsm4(base + L.k + row * 128 + (((kk + (lane >> 4)) ^ (row & 7)) << 4), r);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            mma16816<true>(sc[0], qf[kk + j], e4m3x2_to_f16x2(r[2 * j] & 0xffffu), e4m3x2_to_f16x2(r[2 * j] >> 16));
+                            mma16816<true>(sc[1], qf[kk + j], e4m3x2_to_f16x2(r[2 * j + 1] & 0xffffu), e4m3x2_to_f16x2(r[2 * j + 1] >> 16));
+                        }
+                    }
+                } else {
+                    const int row = key0 + (lane & 7) + ((lane >> 4) << 3);
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk) {
+                        uint32_t r[4];
+                        const int chunk = kk * 2 + ((lane >> 3) & 1);
+                        ldsm4(base + L.k + (chunk >> 3) * 8192 + row * 128 + (((chunk & 7) ^ (row & 7)) << 4), r);
+                        mma16816<false>(sc[0], qf[kk], r[0], r[1]);
+                        mma16816<false>(sc[1], qf[kk], r[2], r[3]);
+                    }
+                }
+                // This thread's scores: rows r4 and r4 + 8, positions key0 + 8 j + 2 t4 + {0, 1}.
+                float vscale[4] = {1.f, 1.f, 1.f, 1.f};
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int key = 8 * j + 2 * t4 + e;
+                        float ks = 1.f;
+                        if (kE4m3) {
+                            const uint8_t *sb = smem + s * L.bytes;
+                            ks = power_of_two(sb[L.ks + key0 + key]);
+                            // Past the end the byte may be anything, and 0 x infinity is NaN.
+                            vscale[2 * j + e] = key < valid ? power_of_two(sb[L.vs + key0 + key]) : 0.f;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            sc[j][2 * i + e] = key < valid ? sc[j][2 * i + e] * (kE4m3 ? qs[i] * ks : qs[i]) : -INFINITY;
+                    }
+                float mn[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    mn[i] = fmaxf(fmaxf(sc[0][2 * i], sc[0][2 * i + 1]), fmaxf(sc[1][2 * i], sc[1][2 * i + 1]));
+                    mn[i] = fmaxf(mn[i], __shfl_xor_sync(0xffffffffu, mn[i], 1));
+                    mn[i] = fmaxf(mn[i], __shfl_xor_sync(0xffffffffu, mn[i], 2));
+                    mn[i] = fmaxf(mn[i], m[i]);
+                }
+                if (__any_sync(0xffffffffu, mn[0] > m[0] || mn[1] > m[1])) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float f = mn[i] == m[i] ? 1.f : ptx::ex2_approx(m[i] - mn[i]);
+                        l[i] *= f;
+                        m[i] = mn[i];
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) {
+                            acc[c][2 * i] *= f;
+                            acc[c][2 * i + 1] *= f;
+                        }
+                    }
+                }
+                uint32_t pf[4];
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float ref = m[i] == -INFINITY ? 0.f : m[i];
+                        const float p0 = ptx::ex2_approx(sc[j][2 * i] - ref), p1 = ptx::ex2_approx(sc[j][2 * i + 1] - ref);
+                        l[i] += p0 + p1;
+                        pf[2 * j + i] = kE4m3 ? pack_bf16(p0 * vscale[2 * j], p1 * vscale[2 * j + 1]) : pack_bf16(p0, p1);
+                    }
+                // Positions past the end hold anything: their value rows count as zero.
+                const uint32_t keep0 = (2 * t4 < valid ? 0xffffu : 0u) | (2 * t4 + 1 < valid ? 0xffff0000u : 0u);
+                const uint32_t keep1 = (2 * t4 + 8 < valid ? 0xffffu : 0u) | (2 * t4 + 9 < valid ? 0xffff0000u : 0u);
+                const int row = key0 + (lane & 15);
+                if (kE4m3) {
+                    // Matrices: keys 0-7 and 8-15 of a 16-byte chunk, then of the next.  A thread gets
+                    // columns 2 r4, 2 r4 + 1 of keys 2 t4, 2 t4 + 1: the even columns make one
+                    // instruction's operand, the odd ones another's.
+#pragma unroll
+                    for (int c = 0; c < 8; c += 2) {
+                        uint32_t r[4];
+                        ldsm4_t(base + L.v + row * 128 + (((c + (lane >> 4)) ^ (row & 7)) << 4), r);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const uint32_t x = __byte_perm(r[2 * j], 0, 0x3120), y = __byte_perm(r[2 * j + 1], 0, 0x3120);
+                            mma16816<false>(acc[2 * (c + j)], pf, e4m3x2_to_bf16x2(x & 0xffffu) & keep0,
+                                            e4m3x2_to_bf16x2(y & 0xffffu) & keep1);
+                            mma16816<false>(acc[2 * (c + j) + 1], pf, e4m3x2_to_bf16x2(x >> 16) & keep0,
+                                            e4m3x2_to_bf16x2(y >> 16) & keep1);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        uint32_t r[4];
+                        const int chunk = 2 * c + (lane >> 4);
+                        ldsm4_t(base + L.v + (chunk >> 3) * 8192 + row * 128 + (((chunk & 7) ^ (row & 7)) << 4), r);
+                        mma16816<false>(acc[2 * c], pf, r[0] & keep0, r[1] & keep1);
+                        mma16816<false>(acc[2 * c + 1], pf, r[2] & keep0, r[3] & keep1);
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(empty(s)) : "memory");
+            ++taken;
+            --left;
+            const bool last = left == 0 || blk + 1 == nb;
+            if (left > 0) advance();
+            if (last) break;
+        }
+        // Join the four warps: each leaves its rows, then a thread takes one column.
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+            const int r = r4 + 8 * i;
+            if (r >= rows) continue;
+            if (t4 == 0) ml_s[warp][r] = make_float2(m[i], l[i]);
+            float *dst = joined + ((size_t)warp * a.rows + r) * kD;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                if (kE4m3) {
+                    // Columns 16 c + 4 t4 + {0, 2} and {1, 3}.
+                    *reinterpret_cast<float4 *>(dst + 16 * c + 4 * t4) =
+                        make_float4(acc[2 * c][2 * i], acc[2 * c + 1][2 * i], acc[2 * c][2 * i + 1], acc[2 * c + 1][2 * i + 1]);
+                } else {
+                    *reinterpret_cast<float2 *>(dst + 16 * c + 2 * t4) = make_float2(acc[2 * c][2 * i], acc[2 * c][2 * i + 1]);
+                    *reinterpret_cast<float2 *>(dst + 16 * c + 8 + 2 * t4) = make_float2(acc[2 * c + 1][2 * i], acc[2 * c + 1][2 * i + 1]);
+                }
+            }
+        }
+        asm volatile("bar.sync 1, %0;" ::"n"(kComputeWarps * 32) : "memory");
+        if (!aborted) {
+            const size_t slot = (size_t)blockIdx.x * 2 + piece;
+            for (int r = 0; r < rows; ++r) {
+                float M = -INFINITY, den = 0.f, x = 0.f;
+#pragma unroll
+                for (int w = 0; w < kComputeWarps; ++w) M = fmaxf(M, ml_s[w][r].x);
+#pragma unroll
+                for (int w = 0; w < kComputeWarps; ++w) {
+                    const float2 ml = ml_s[w][r];
+                    const float f = ml.x == -INFINITY ? 0.f : ptx::ex2_approx(ml.x - M);
+                    x = fmaf(f, joined[((size_t)w * a.rows + r) * kD + tid], x);
+                    den = fmaf(f, ml.y, den);
+                }
+                if (!whole) {
+                    a.part_o[(slot * a.rows + r) * kD + tid] = x;
+                    if (tid == 0) a.part_ml[slot * a.rows + r] = make_float2(M, any_bad ? -1.f : den);
+                } else if (!any_bad) {
+                    a.o[((size_t)cb * a.heads_q + head0 + r) * kD + tid] = __float2bfloat16_rn(den > 0.f ? x / den : x);
+                }
+            }
+        }
+        // All four warps leave together when one of them has given up waiting.
+        uint32_t stop;
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t"
+            "setp.ne.u32 q, %1, 0;\n\t"
+            "bar.red.or.pred p, 1, %2, q;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(stop)
+            : "r"(run && !aborted ? 0u : 1u), "n"(kComputeWarps * 32)
+            : "memory");
+        if (stop) break;
+        piece = 1;
+    }
+}
+
+// Joins the pieces of every row of blocks that more than one share holds.  One block per
+// (sequence, key/value head, row tile); a warp per query head, four columns per lane.
+__global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const PagedArgs a)
+{
+    __shared__ int tmp[33];
+    __shared__ int before_s;
+    pdl_start();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per_seq = a.heads_kv * a.row_tiles;
+    const int item = blockIdx.x % per_seq, b = blockIdx.x / per_seq;
+    int n_all = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += kCombineThreads) {
+        int t;
+        const int before = block_scan(b0 + tid < a.batch ? blocks_of(a, b0 + tid) : 0, tmp, &t);
+        if (b0 + tid == b) before_s = n_all + before;
+        n_all += t;
+    }
+    __syncthreads();
+    const int nb = blocks_of(a, b);
+    if (nb == 0) return;
+    const long long total = (long long)n_all * per_seq;
+    const long long begin = (long long)before_s * per_seq + (long long)item * nb, end = begin + nb;
+    // The share that holds block x: the last c with share_begin(c) <= x.
+    const int shares = (int)min((long long)a.shares, total);
+    const int c0 = (int)(((begin + 1) * shares - 1) / total), c1 = (int)((end * shares - 1) / total);
+    if (c0 == c1) return;
+    const int first = share_begin(total, c0, shares) == begin ? 0 : 1;
+    const int hkv = item / a.row_tiles, rt = item % a.row_tiles;
+    const int rows = min(kHeadRows, a.group - rt * kHeadRows);
+    for (int r = warp; r < rows; r += kCombineThreads / 32) {
+        float M = -INFINITY, den = 0.f;
+        bool bad = false;
+        for (int c = c0 + lane; c <= c1; c += 32) {
+            const float2 ml = a.part_ml[((size_t)c * 2 + (c == c0 ? first : 0)) * a.rows + r];
+            M = fmaxf(M, ml.x);
+            bad |= ml.y < 0.f;
+        }
+        if (__any_sync(0xffffffffu, bad)) continue;
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = c0; c <= c1; ++c) {
+            const size_t at = ((size_t)c * 2 + (c == c0 ? first : 0)) * a.rows + r;
+            const float2 ml = a.part_ml[at];
+            const float f = ml.x == -INFINITY ? 0.f : ptx::ex2_approx(ml.x - M);
+            const float4 v = reinterpret_cast<const float4 *>(a.part_o + at * kD)[lane];
+            x.x = fmaf(f, v.x, x.x);
+            x.y = fmaf(f, v.y, x.y);
+            x.z = fmaf(f, v.z, x.z);
+            x.w = fmaf(f, v.w, x.w);
+            den = fmaf(f, ml.y, den);
+        }
+        const float inv = den > 0.f ? 1.f / den : 1.f;
+        uint2 w = make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
+        reinterpret_cast<uint2 *>(a.o + ((size_t)b * a.heads_q + hkv * a.group + rt * kHeadRows + r) * kD)[lane] = w;
+    }
+}
+
+constexpr int kMaxDevices = 64;
+std::mutex g_mutex;
+int g_sms[kMaxDevices] = {};
+
+cudaError_t prepare(int *sms)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(g_mutex);
+    if (!g_sms[dev]) {
+        if ((e = cudaFuncSetAttribute(paged_attention_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerCta)) != cudaSuccess ||
+            (e = cudaFuncSetAttribute(paged_attention_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerCta)) != cudaSuccess)
+            return e;
+        int n = 0;
+        if ((e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+        g_sms[dev] = n > 0 ? n : 1;
+    }
+    *sms = g_sms[dev];
+    return cudaSuccess;
+}
+
+bool heads_ok(int heads_q, int heads_kv) { return heads_q >= 1 && heads_kv >= 1 && heads_q % heads_kv == 0; }
+
+size_t paged_ws(int shares, int rows) { return (size_t)shares * 2 * rows * (kD * sizeof(float) + sizeof(float2)); }
+
+bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+}  // namespace
+}  // namespace stree
+
+using namespace stree;
+
+extern "C" stree_status stree_paged_attention_workspace_size(int heads_q, int heads_kv, int head_dim, size_t *bytes)
+{
+    if (!bytes) return STREE_ERR_INVALID_ARG;
+    if (!heads_ok(heads_q, heads_kv) || head_dim != kD) return STREE_ERR_UNSUPPORTED;
+    int sms = 0;
+    if (prepare(&sms) != cudaSuccess) return STREE_ERR_CUDA;
+    const int group = heads_q / heads_kv;
+    *bytes = paged_ws(2 * sms, group < kHeadRows ? group : kHeadRows);
+    return STREE_OK;
+}
+
+extern "C" stree_status stree_paged_attention(const void *q, const void *k_pages, const void *v_pages,
+                                              const uint8_t *k_scales, const uint8_t *v_scales,
+                                              const int32_t *page_table, const int32_t *seq_len, int batch,
+                                              int heads_q, int heads_kv, int head_dim, int n_pages, int page_size,
+                                              int max_pages, float scale, stree_dtype dtype, stree_dtype cache_dtype,
+                                              void *o, void *workspace, size_t workspace_bytes, int32_t *err_out,
+                                              void *stream)
+{
+    if (!heads_ok(heads_q, heads_kv) || dtype != STREE_BF16) return STREE_ERR_UNSUPPORTED;
+    stree_status st = check_cache(k_pages, v_pages, k_scales, v_scales, page_table, batch, heads_kv, head_dim, n_pages,
+                                  page_size, max_pages, cache_dtype);
+    if (st != STREE_OK) return st;
+    if (!(scale > 0.f)) return STREE_ERR_INVALID_ARG;
+    if (batch == 0) return STREE_OK;
+    if (!q || !seq_len || !o || !workspace) return STREE_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(o, 16) || !aligned(workspace, 16) || !aligned(seq_len, 4) || !aligned(err_out, 4))
+        return STREE_ERR_MISALIGNED;
+    PagedArgs a{};
+    a.group = heads_q / heads_kv;
+    a.rows = a.group < kHeadRows ? a.group : kHeadRows;
+    a.row_tiles = (a.group + kHeadRows - 1) / kHeadRows;
+    const long long blocks = ((long long)max_pages * page_size + kBlk - 1) / kBlk;
+    if (blocks * batch > 0x7fffffffLL || (long long)batch * heads_kv * a.row_tiles > 0x7fffffffLL)
+        return STREE_ERR_UNSUPPORTED;
+    int sms = 0;
+    if (prepare(&sms) != cudaSuccess) return STREE_ERR_CUDA;
+    // As many shares as the SMs hold CTAs, and no more than there can be blocks.
+    const long long most = blocks * batch * heads_kv * a.row_tiles;
+    a.shares = (int)(most < 2LL * sms ? most : 2LL * sms);
+    const size_t need = paged_ws(a.shares, a.rows);
+    if (workspace_bytes < need) return STREE_ERR_INVALID_ARG;
+    const bool e4m3 = cache_dtype == STREE_E4M3;
+    a.box_rows = 8;
+    while (a.box_rows < kBlk && page_size % (2 * a.box_rows) == 0) a.box_rows *= 2;
+    const long long rows = (long long)n_pages * heads_kv * page_size;
+    CUtensorMap m_k, m_v;
+    if (!encode_rows(&m_k, k_pages, e4m3, rows, a.box_rows) || !encode_rows(&m_v, v_pages, e4m3, rows, a.box_rows))
+        return STREE_ERR_CUDA;
+    a.q = static_cast<const __nv_bfloat16 *>(q);
+    a.k_scales = k_scales;
+    a.v_scales = v_scales;
+    a.table = page_table;
+    a.lens = seq_len;
+    a.o = static_cast<__nv_bfloat16 *>(o);
+    a.part_o = static_cast<float *>(workspace);
+    a.part_ml = reinterpret_cast<float2 *>(a.part_o + (size_t)a.shares * 2 * a.rows * kD);
+    a.err = err_out;
+    a.batch = batch;
+    a.heads_q = heads_q;
+    a.heads_kv = heads_kv;
+    a.n_pages = n_pages;
+    a.page_size = page_size;
+    a.max_pages = max_pages;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    const int stage = e4m3 ? stage_layout<true>().bytes : stage_layout<false>().bytes;
+    const int join = kComputeWarps * a.rows * kD * (int)sizeof(float), slack = 1024, fixed = 2048;
+    a.stages = (kSmemPerCta - join - slack - fixed) / stage;
+    if (a.stages > kMaxStages) a.stages = kMaxStages;
+    const size_t smem = (size_t)a.stages * stage + join + slack;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = launch_pdl(e4m3 ? paged_attention_kernel<true> : paged_attention_kernel<false>,
+                                     dim3((unsigned)a.shares + 1), kThreads, smem, s, m_k, m_v, a);
+    if (e != cudaSuccess) return STREE_ERR_CUDA;
+    return launch_pdl(paged_combine_kernel, dim3((unsigned)(batch * heads_kv * a.row_tiles)), kCombineThreads, 0, s, a) ==
+                   cudaSuccess
+               ? STREE_OK
+               : STREE_ERR_CUDA;
+}

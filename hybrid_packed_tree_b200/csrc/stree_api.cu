@@ -437,6 +437,8 @@ const char *stree_status_string(stree_status st)
     case STREE_ERR_CUDA: return "CUDA runtime error";
     case STREE_ERR_TIMEOUT: return "device wait timed out";
     case STREE_ERR_NO_TREE: return "no tree or scan recorded for these sizes";
+    case STREE_ERR_BAD_SEQ: return "sequence offsets are not ascending within the packed rows";
+    case STREE_ERR_BAD_PAGE: return "page out of range, or tokens past the end of a page table";
     }
     return "unknown status";
 }

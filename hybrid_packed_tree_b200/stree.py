@@ -29,9 +29,9 @@ STREE_OK = 0
 STATUS_NAMES = {
     0: "STREE_OK", 1: "STREE_ERR_INVALID_ARG", 2: "STREE_ERR_UNSUPPORTED", 3: "STREE_ERR_BAD_TREE",
     4: "STREE_ERR_BAD_PATH", 5: "STREE_ERR_MISALIGNED", 6: "STREE_ERR_CUDA", 7: "STREE_ERR_TIMEOUT",
-    8: "STREE_ERR_NO_TREE",
+    8: "STREE_ERR_NO_TREE", 9: "STREE_ERR_BAD_SEQ", 10: "STREE_ERR_BAD_PAGE",
 }
-STREE_F32, STREE_BF16 = 0, 1
+STREE_F32, STREE_BF16, STREE_E4M3 = 0, 1, 2
 KERNELS = {"auto": 0, "simt": 1, "tc": 2, "small": 3}
 
 # Every exported symbol of include/stree.h.
@@ -42,6 +42,9 @@ EXPORTS = (
     "stree_tree_scan", "stree_commit", "stree_tree_scan_commit", "stree_tree_scan_commit_noalloc",
     "stree_resolve_path", "stree_unrolled_scan", "stree_accept_greedy", "stree_accept_sampling",
     "stree_gdn_tree_scan_commit", "stree_tree_attention", "stree_tree_attention_workspace_size",
+    "stree_linear_prompt", "stree_linear_prompt_workspace_size", "stree_linear_step", "stree_prompt_attention",
+    "stree_paged_attention", "stree_paged_attention_workspace_size", "stree_cache_write", "stree_cache_commit",
+    "stree_cache_read",
     "stree_sync_check", "stree_status_string", "stree_version",
 )
 
@@ -66,6 +69,16 @@ _lib.stree_accept_sampling.argtypes = [_vp, _vp, _i, _i, _vp, _vp, _i, _i, ctype
 _lib.stree_gdn_tree_scan_commit.argtypes = [_vp] * 8 + [_i] * 7 + [_vp, _vp, _i, _vp, _vp, _vp, _vp]
 _lib.stree_tree_attention.argtypes = [_vp] * 7 + [_i] * 6 + [ctypes.c_float, _i, _vp, _vp, ctypes.c_size_t, _vp, _vp]
 _lib.stree_tree_attention_workspace_size.argtypes = [_i] * 6 + [ctypes.POINTER(ctypes.c_size_t)]
+_lib.stree_linear_prompt.argtypes = [_vp] * 8 + [_i] * 7 + [_vp, _vp, _vp, ctypes.c_size_t, _vp, _vp]
+_lib.stree_linear_prompt_workspace_size.argtypes = [_i] * 7 + [ctypes.POINTER(ctypes.c_size_t)]
+_lib.stree_linear_step.argtypes = [_vp] * 7 + [_i] * 6 + [_vp, _vp, _vp]
+_lib.stree_prompt_attention.argtypes = [_vp] * 4 + [_i] * 5 + [ctypes.c_float, _i, _vp, _vp, _vp]
+_lib.stree_paged_attention.argtypes = [_vp] * 7 + [_i] * 7 + [ctypes.c_float, _i, _i, _vp, _vp, ctypes.c_size_t, _vp,
+                                                                _vp]
+_lib.stree_paged_attention_workspace_size.argtypes = [_i] * 3 + [ctypes.POINTER(ctypes.c_size_t)]
+_lib.stree_cache_write.argtypes = [_vp] * 5 + [_i] * 9 + [_vp] * 6
+_lib.stree_cache_commit.argtypes = [_vp] * 4 + [_i, _vp, _vp] + [_i] * 9 + [_vp] * 6
+_lib.stree_cache_read.argtypes = [_vp] * 6 + [_i] * 9 + [_vp] * 4
 _lib.stree_sync_check.argtypes = [_vp, _vp, _ip]
 _lib.stree_status_string.argtypes = [_i]
 _lib.stree_status_string.restype = ctypes.c_char_p
@@ -358,6 +371,200 @@ def stree_tree_attention(q, k_ctx, v_ctx, k_tree, v_tree, ctx_len, parent, o, sc
                                    _ptr(err_out, "err_out", (torch.int32,)), _stream(stream))
     _check(st, "stree_tree_attention")
     return o
+
+
+# ---------------------------------------------------------------- prompts, single tokens, the paged cache
+
+_F32, _BF16 = (torch.float32,), (torch.bfloat16,)
+_I32, _U8 = (torch.int32,), (torch.uint8,)
+
+
+def _want(t, name, shape, like):
+    """Shape and device of an argument of the calls below (None passes)."""
+    if t is None:
+        return
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+
+
+def _call(where, fn, like, stream, *args):
+    """Calls a library function on the device of `like`, on its current stream when none is given."""
+    if like.device.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(stream)), where)
+        return
+    with torch.cuda.device(like.device):
+        _check(fn(*args, _stream(stream)), where)
+
+
+def _scratch(workspace, like):
+    if workspace is None:
+        return None, 0
+    if not isinstance(workspace, torch.Tensor) or workspace.device != like.device:
+        raise ValueError(f"workspace must be a tensor on {like.device}")
+    return _ptr(workspace, "workspace", _U8), workspace.numel()
+
+
+def stree_linear_prompt_workspace_size(batch, total, heads_v, heads_k, dk, dv, dtype=torch.bfloat16) -> int:
+    """Bytes of the workspace in which stree_linear_prompt splits long sequences on the current device (0: no split)."""
+    n = ctypes.c_size_t(0)
+    code = {torch.float32: STREE_F32, torch.bfloat16: STREE_BF16}.get(dtype, -1)
+    _check(_lib.stree_linear_prompt_workspace_size(int(batch), int(total), int(heads_v), int(heads_k), int(dk), int(dv),
+                                                   code, ctypes.byref(n)), "stree_linear_prompt_workspace_size")
+    return int(n.value)
+
+
+def stree_linear_prompt(q, k, v, alpha, beta, cu_seqlens, o, S0=None, S_new=None, skip=None, err_out=None,
+                        workspace=None, stream=None):
+    """Linear attention with a decay for each head over packed prompts: o [total, Hv, dv] and, when
+    S_new is given, the states [b, Hv, dv, dk] after the last tokens.  q, k [total, Hk, dk] and v in
+    one dtype (fp32 or bf16); alpha, beta [total, Hv] fp32 (beta None: ones); S0 fp32 (None: zeros);
+    skip [Hv] fp32 or None; cu_seqlens [b + 1] int32.  workspace: a device uint8 tensor of
+    stree_linear_prompt_workspace_size() bytes, or None (long sequences are not split)."""
+    total, Hk, dk = k.shape
+    Hv, dv = v.shape[1], v.shape[2]
+    batch = cu_seqlens.shape[0] - 1
+    _want(cu_seqlens, "cu_seqlens", (batch + 1,), v)
+    for t, name, shape in ((q, "q", (total, Hk, dk)), (k, "k", (total, Hk, dk)), (v, "v", (total, Hv, dv)),
+                           (o, "o", (total, Hv, dv)), (alpha, "alpha", (total, Hv)), (beta, "beta", (total, Hv)),
+                           (S0, "S0", (batch, Hv, dv, dk)), (S_new, "S_new", (batch, Hv, dv, dk)), (skip, "skip", (Hv,)),
+                           (err_out, "err_out", (4,))):
+        _want(t, name, shape, v)
+    io = (v.dtype,)
+    ws, ws_bytes = _scratch(workspace, v)
+    _call("stree_linear_prompt", _lib.stree_linear_prompt, v, stream, _ptr(q, "q", io), _ptr(k, "k", io),
+          _ptr(v, "v", _F32 + _BF16), _ptr(alpha, "alpha", _F32), _ptr(beta, "beta", _F32), _ptr(skip, "skip", _F32),
+          _ptr(S0, "S0", _F32), _ptr(cu_seqlens, "cu_seqlens", _I32), total, batch, Hv, Hk, dk, dv, _io_dtype(v),
+          _ptr(o, "o", io), _ptr(S_new, "S_new", _F32), ws, ws_bytes, _ptr(err_out, "err_out", _I32))
+    return o, S_new
+
+
+def stree_linear_step(q, k, v, alpha, beta, S0, o, S_new, skip=None, stream=None):
+    """One token of stree_linear_prompt's recurrence for every sequence: (o [b, Hv, dv], S_new) from
+    q, k [b, Hk, dk], v [b, Hv, dv], alpha, beta [b, Hv] (beta None: ones) and S0 (S_new may be S0)."""
+    batch, Hk, dk = k.shape
+    Hv, dv = v.shape[1], v.shape[2]
+    for t, name, shape in ((q, "q", (batch, Hk, dk)), (k, "k", (batch, Hk, dk)), (v, "v", (batch, Hv, dv)),
+                           (o, "o", (batch, Hv, dv)), (alpha, "alpha", (batch, Hv)), (beta, "beta", (batch, Hv)),
+                           (S0, "S0", (batch, Hv, dv, dk)), (S_new, "S_new", (batch, Hv, dv, dk)), (skip, "skip", (Hv,))):
+        _want(t, name, shape, v)
+    io = (v.dtype,)
+    _call("stree_linear_step", _lib.stree_linear_step, v, stream, _ptr(q, "q", io), _ptr(k, "k", io),
+          _ptr(v, "v", _F32 + _BF16), _ptr(alpha, "alpha", _F32), _ptr(beta, "beta", _F32), _ptr(skip, "skip", _F32),
+          _ptr(S0, "S0", _F32), batch, Hv, Hk, dk, dv, _io_dtype(v), _ptr(o, "o", io), _ptr(S_new, "S_new", _F32))
+    return o, S_new
+
+
+def stree_prompt_attention(q, k, v, cu_seqlens, o, scale, err_out=None, stream=None):
+    """Causal attention over packed prompts: o [total, Hq, 128] from q, k, v [total, H, 128] (bf16) and
+    cu_seqlens [b + 1] int32."""
+    total, Hq, d = q.shape
+    Hkv = k.shape[1]
+    batch = cu_seqlens.shape[0] - 1
+    for t, name, shape in ((q, "q", (total, Hq, d)), (k, "k", (total, Hkv, d)), (v, "v", (total, Hkv, d)),
+                           (o, "o", (total, Hq, d)), (cu_seqlens, "cu_seqlens", (batch + 1,)), (err_out, "err_out", (4,))):
+        _want(t, name, shape, q)
+    _call("stree_prompt_attention", _lib.stree_prompt_attention, q, stream, _ptr(q, "q", _BF16), _ptr(k, "k", _BF16),
+          _ptr(v, "v", _BF16), _ptr(cu_seqlens, "cu_seqlens", _I32), total, batch, Hq, Hkv, d, float(scale), STREE_BF16,
+          _ptr(o, "o", _BF16), _ptr(err_out, "err_out", _I32))
+    return o
+
+
+def _cache(k_pages, v_pages, page_table, k_scales, v_scales, like):
+    """Pointers and sizes of a paged cache: (k, v, k scales, v scales, table), (n_pages, page size,
+    pages per sequence), its dtype code, heads and head dim."""
+    n_pages, Hkv, page, d = k_pages.shape
+    batch, max_pages = page_table.shape
+    for t, name, shape in ((k_pages, "k_pages", (n_pages, Hkv, page, d)), (v_pages, "v_pages", (n_pages, Hkv, page, d)),
+                           (page_table, "page_table", (batch, max_pages)), (k_scales, "k_scales", (n_pages, Hkv, page)),
+                           (v_scales, "v_scales", (n_pages, Hkv, page))):
+        _want(t, name, shape, like)
+    e4m3 = k_pages.dtype == torch.float8_e4m3fn
+    pages = (torch.float8_e4m3fn,) if e4m3 else _BF16
+    if e4m3 != (k_scales is not None) or e4m3 != (v_scales is not None):
+        raise ValueError("k_scales and v_scales go with float8_e4m3fn pages, and with them alone")
+    return ((_ptr(k_pages, "k_pages", pages), _ptr(v_pages, "v_pages", pages), _ptr(k_scales, "k_scales", _U8),
+             _ptr(v_scales, "v_scales", _U8), _ptr(page_table, "page_table", _I32)), (n_pages, page, max_pages),
+            STREE_E4M3 if e4m3 else STREE_BF16, Hkv, d)
+
+
+def stree_paged_attention_workspace_size(heads_q, heads_kv, head_dim=128) -> int:
+    """Bytes of stree_paged_attention's workspace on the current device (any batch and length)."""
+    n = ctypes.c_size_t(0)
+    _check(_lib.stree_paged_attention_workspace_size(int(heads_q), int(heads_kv), int(head_dim), ctypes.byref(n)),
+           "stree_paged_attention_workspace_size")
+    return int(n.value)
+
+
+def stree_paged_attention(q, k_pages, v_pages, page_table, seq_len, o, scale, k_scales=None, v_scales=None,
+                          err_out=None, workspace=None, stream=None):
+    """One new token per sequence over its paged cache: o [b, Hq, 128] (bf16) from q [b, Hq, 128],
+    pages [n, Hkv, page, 128] (bf16, or float8_e4m3fn with uint8 scales [n, Hkv, page]), page_table
+    [b, max_pages] and seq_len [b] int32.  workspace: a device uint8 tensor of
+    stree_paged_attention_workspace_size() bytes."""
+    batch, Hq, d = q.shape
+    ptrs, sizes, code, Hkv, dc = _cache(k_pages, v_pages, page_table, k_scales, v_scales, q)
+    for t, name, shape in ((q, "q", (batch, Hq, dc)), (o, "o", (batch, Hq, d)), (seq_len, "seq_len", (batch,)),
+                           (page_table, "page_table", (batch, sizes[2])), (err_out, "err_out", (4,))):
+        _want(t, name, shape, q)
+    ws, ws_bytes = _scratch(workspace, q)
+    _call("stree_paged_attention", _lib.stree_paged_attention, q, stream, _ptr(q, "q", _BF16), *ptrs,
+          _ptr(seq_len, "seq_len", _I32), batch, Hq, Hkv, d, *sizes, float(scale), STREE_BF16, code, _ptr(o, "o", _BF16),
+          ws, ws_bytes, _ptr(err_out, "err_out", _I32))
+    return o
+
+
+def stree_cache_write(k, v, cu_seqlens, start, page_table, k_pages, v_pages, k_scales=None, v_scales=None,
+                      err_out=None, stream=None):
+    """Writes packed new keys and values k, v [total, Hkv, 128] (bf16) into the pages, token i of
+    sequence b at position start[b] + i; quantised as they are written when the pages are
+    float8_e4m3fn (one power-of-two scale per row, in k_scales and v_scales)."""
+    ptrs, sizes, code, Hkv, d = _cache(k_pages, v_pages, page_table, k_scales, v_scales, k)
+    total, batch = k.shape[0], page_table.shape[0]
+    for t, name, shape in ((k, "k", (total, Hkv, d)), (v, "v", (total, Hkv, d)), (cu_seqlens, "cu_seqlens", (batch + 1,)),
+                           (start, "start", (batch,)), (err_out, "err_out", (4,))):
+        _want(t, name, shape, k)
+    _call("stree_cache_write", _lib.stree_cache_write, k, stream, _ptr(k, "k", _BF16), _ptr(v, "v", _BF16),
+          _ptr(cu_seqlens, "cu_seqlens", _I32), _ptr(start, "start", _I32), ptrs[4], total, batch, Hkv, d, *sizes,
+          STREE_BF16, code, *ptrs[:4], _ptr(err_out, "err_out", _I32))
+    return k_pages, v_pages
+
+
+def stree_cache_commit(k_tree, v_tree, path, path_len, start, page_table, k_pages, v_pages, k_scales=None,
+                       v_scales=None, err_out=None, stream=None):
+    """Writes the accepted path of each tree into the pages: node path[b, i] of k_tree, v_tree
+    [b, T, Hkv, 128] (bf16) at position start[b] + i, i < path_len[b]."""
+    ptrs, sizes, code, Hkv, d = _cache(k_pages, v_pages, page_table, k_scales, v_scales, k_tree)
+    batch, T = k_tree.shape[:2]
+    maxlen = path.shape[1]
+    for t, name, shape in ((k_tree, "k_tree", (batch, T, Hkv, d)), (v_tree, "v_tree", (batch, T, Hkv, d)),
+                           (path, "path", (batch, maxlen)), (path_len, "path_len", (batch,)), (start, "start", (batch,)),
+                           (page_table, "page_table", (batch, sizes[2])), (err_out, "err_out", (4,))):
+        _want(t, name, shape, k_tree)
+    _call("stree_cache_commit", _lib.stree_cache_commit, k_tree, stream, _ptr(k_tree, "k_tree", _BF16),
+          _ptr(v_tree, "v_tree", _BF16), _ptr(path, "path", _I32), _ptr(path_len, "path_len", _I32), maxlen,
+          _ptr(start, "start", _I32), ptrs[4], T, batch, Hkv, d, *sizes, STREE_BF16, code, *ptrs[:4],
+          _ptr(err_out, "err_out", _I32))
+    return k_pages, v_pages
+
+
+def stree_cache_read(k_pages, v_pages, page_table, seq_len, k_ctx, v_ctx, k_scales=None, v_scales=None, err_out=None,
+                     stream=None):
+    """Reads the first seq_len[b] positions of the pages back into the contiguous cache of
+    stree_tree_attention, k_ctx, v_ctx [b, S, Hkv, 128] (bf16); later positions are untouched."""
+    ptrs, sizes, code, Hkv, d = _cache(k_pages, v_pages, page_table, k_scales, v_scales, k_ctx)
+    batch, S = k_ctx.shape[:2]
+    for t, name, shape in ((k_ctx, "k_ctx", (batch, S, Hkv, d)), (v_ctx, "v_ctx", (batch, S, Hkv, d)),
+                           (seq_len, "seq_len", (batch,)), (page_table, "page_table", (batch, sizes[2])),
+                           (err_out, "err_out", (4,))):
+        _want(t, name, shape, k_ctx)
+    _call("stree_cache_read", _lib.stree_cache_read, k_ctx, stream, *ptrs, _ptr(seq_len, "seq_len", _I32), batch, S, Hkv,
+          d, *sizes, code, STREE_BF16, _ptr(k_ctx, "k_ctx", _BF16), _ptr(v_ctx, "v_ctx", _BF16),
+          _ptr(err_out, "err_out", _I32))
+    return k_ctx, v_ctx
 
 
 def stree_resolve_path(ctx: Ctx, path, path_len, leaf_out, stream=None):

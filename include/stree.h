@@ -84,11 +84,15 @@ typedef enum {
     STREE_ERR_MISALIGNED = 5,   /* a tensor pointer is not 16-byte aligned */
     STREE_ERR_CUDA = 6,         /* a CUDA runtime call failed (launch, allocation) */
     STREE_ERR_TIMEOUT = 7,      /* a bounded wait inside the tensor-core kernel gave up (about 1 s) */
-    STREE_ERR_NO_TREE = 8       /* scan with parent = NULL before any tree was built, or
+    STREE_ERR_NO_TREE = 8,      /* scan with parent = NULL before any tree was built, or
                                    commit before any scan, or a size mismatch with them */
+    STREE_ERR_BAD_SEQ = 9,      /* device-detected: packed offsets not ascending in [0, total] */
+    STREE_ERR_BAD_PAGE = 10     /* device-detected: a used page id is out of range, or tokens
+                                   do not fit their page table */
 } stree_status;
 
-typedef enum { STREE_F32 = 0, STREE_BF16 = 1 } stree_dtype;
+/* STREE_E4M3 is a type of cache pages only. */
+typedef enum { STREE_F32 = 0, STREE_BF16 = 1, STREE_E4M3 = 2 } stree_dtype;
 
 /* Which scan kernel a context uses (stree_ctx_set_kernel). */
 typedef enum {
@@ -387,6 +391,149 @@ stree_status stree_tree_attention(const void *q, const void *k_ctx, const void *
  */
 stree_status stree_tree_attention_workspace_size(int n_nodes, int batch, int ctx_cap, int heads_q, int heads_kv,
                                                  int head_dim, size_t *bytes);
+
+/*
+ * Prompts and single tokens of the same layers (what makes the state and the cache
+ * that the tree calls above start from).  Common to the calls below:
+ *
+ *   Packed sequences: the rows of `batch` sequences one behind the other; sequence b
+ *   has rows cu_seqlens[b] .. cu_seqlens[b+1] - 1 (device int32 [batch + 1], ascending
+ *   in [0, total]; equal entries are an empty sequence).  Rows behind the last sequence
+ *   are neither read into a result nor written.  A sequence whose pair of offsets is not
+ *   ascending in [0, total] counts as empty and latches STREE_ERR_BAD_SEQ.
+ *
+ *   Paged cache: k_pages, v_pages [n_pages, heads_kv, page_size, 128]; position j of
+ *   sequence b is row j % page_size of page page_table[b][j / page_size] (device int32
+ *   [batch, max_pages]; entries past a sequence's last page are not read).  Pages are
+ *   bf16 (scales NULL) or e4m3 with k_scales, v_scales uint8 [n_pages, heads_kv,
+ *   page_size], the element times 2^(scale - 127) being the value.  page_size is a
+ *   multiple of 8 up to 4096, n_pages * heads_kv * page_size below 2^31.  A page id
+ *   outside [0, n_pages), or tokens that do not fit max_pages pages, latch
+ *   STREE_ERR_BAD_PAGE; no memory outside the pages is touched.
+ *
+ *   err_out: device int32[4] error word of this call (cleared by the call), or NULL to
+ *   discard device-detected errors.  No call allocates; every call runs on `stream`, on
+ *   the current device, and may be captured in a CUDA graph.  A workspace belongs to the
+ *   caller, holds nothing between calls, and may be shared by calls (captured ones
+ *   too) that are ordered.  Inputs must be finite; what lies behind a sequence's end
+ *   or in a cache position that is not valid may be anything.  Outputs must not overlap
+ *   inputs except where a call says so.
+ */
+
+/*
+ * Linear attention with a decay for each head over whole prompts.  Per sequence and
+ * value head h (query/key head h / (heads_v / heads_k)):
+ *     S_t = alpha_t S_{t-1} + beta_t v_t k_t^T,   o_t = S_t q_t + skip_h v_t,
+ * S before the first token S0[b,h].  This is stree_gdn_tree_scan_commit's recurrence at
+ * erase zero along one chain; with q = C, k = B, v = x, alpha = exp(dt A), beta = dt and
+ * skip = D it is the SSM layer's (dv = headdim, dk = dstate, S = h).
+ *
+ *   q, k [total, heads_k, dk], v, o [total, heads_v, dv]  dtype (fp32 or bf16)
+ *   alpha [total, heads_v] fp32 in [0, 1] (0 forgets everything before the token)
+ *   beta  [total, heads_v] fp32, or NULL (ones);  skip [heads_v] fp32, or NULL (none)
+ *   S0    [batch, heads_v, dv, dk] fp32, or NULL (zeros)
+ *   S_new [batch, heads_v, dv, dk] fp32: the state after each sequence's last token (S0 for
+ *         an empty sequence), may be S0 itself; or NULL (not wanted)
+ *   workspace: stree_linear_prompt_workspace_size() bytes, 16-byte aligned, or NULL.  With
+ *         fewer bytes, or none, the call does not split long sequences over CTAs (same
+ *         result up to rounding order, slower on few long sequences).
+ *
+ * Shapes: dk and dv multiples of 8 up to 256, heads_v a multiple of heads_k.  fp32 inputs
+ * and shapes other than those below run on CUDA cores in fp32.  bf16 with dk = 128 and dv =
+ * 128, or dv = 64 with an even number of value heads per key head, runs in chunks of 128
+ * tokens on the tensor cores: the pair weights and the state that a chunk's queries
+ * read are rounded to bf16 (they only enter o, itself bf16); the state itself is
+ * accumulated in fp32 from products exact to 2^-17.
+ */
+stree_status stree_linear_prompt(const void *q, const void *k, const void *v, const float *alpha, const float *beta,
+                                 const float *skip, const float *S0, const int32_t *cu_seqlens, int total, int batch,
+                                 int heads_v, int heads_k, int dk, int dv, stree_dtype dtype, void *o, float *S_new,
+                                 void *workspace, size_t workspace_bytes, int32_t *err_out, void *stream);
+
+/* Workspace bytes that stree_linear_prompt wants for these shapes on the current device
+ * (0 when it does not split). */
+stree_status stree_linear_prompt_workspace_size(int batch, int total, int heads_v, int heads_k, int dk, int dv,
+                                                stree_dtype dtype, size_t *bytes);
+
+/*
+ * One token of the same recurrence for every sequence: q, k [batch, heads_k, dk], v, o
+ * [batch, heads_v, dv], alpha, beta [batch, heads_v], S0 and S_new required (S_new may be
+ * S0).  fp32 arithmetic throughout.  Nothing is checked on the device.
+ */
+stree_status stree_linear_step(const void *q, const void *k, const void *v, const float *alpha, const float *beta,
+                               const float *skip, const float *S0, int batch, int heads_v, int heads_k, int dk, int dv,
+                               stree_dtype dtype, void *o, float *S_new, void *stream);
+
+/*
+ * Causal attention over whole prompts (the Transformer layers of the hybrid model):
+ *     o[t,h] = sum_j softmax_j(scale q[t,h] . k[j,g]) v[j,g],  j <= t of t's sequence,
+ * g = h / (heads_q / heads_kv).  q, o [total, heads_q, 128], k, v [total, heads_kv, 128]
+ * bf16; fp32 scores, softmax and sums, P rounded to bf16 for the second product.
+ * Shapes: head dim 128, up to 128 query heads per key/value head; scale > 0.
+ */
+stree_status stree_prompt_attention(const void *q, const void *k, const void *v, const int32_t *cu_seqlens, int total,
+                                    int batch, int heads_q, int heads_kv, int head_dim, float scale,
+                                    stree_dtype dtype, void *o, int32_t *err_out, void *stream);
+
+/*
+ * Attention of one new token per sequence over its paged cache (the token's own key and
+ * value included: write them first):
+ *     o[b,h] = sum_j softmax_j(scale q[b,h] . k_j) v_j,  j in [0, seq_len[b]).
+ * q, o [batch, heads_q, 128] bf16; seq_len device int32 [batch], clamped to [0, max_pages
+ * page_size]; a sequence with no position gives zeros.  A sequence with a page out of
+ * range among those it uses keeps its o untouched.  Any number of query heads per
+ * key/value head; scale > 0.  fp32 scores, softmax and sums; P (times the value's scale
+ * with e4m3 pages) rounded to bf16.  workspace: stree_paged_attention_workspace_size()
+ * bytes, 16-byte aligned, required.
+ */
+stree_status stree_paged_attention(const void *q, const void *k_pages, const void *v_pages, const uint8_t *k_scales,
+                                   const uint8_t *v_scales, const int32_t *page_table, const int32_t *seq_len,
+                                   int batch, int heads_q, int heads_kv, int head_dim, int n_pages, int page_size,
+                                   int max_pages, float scale, stree_dtype dtype, stree_dtype cache_dtype, void *o,
+                                   void *workspace, size_t workspace_bytes, int32_t *err_out, void *stream);
+
+/* Workspace bytes of stree_paged_attention on the current device (any batch and length). */
+stree_status stree_paged_attention_workspace_size(int heads_q, int heads_kv, int head_dim, size_t *bytes);
+
+/*
+ * Writes new keys and values into the pages: token i of sequence b (packed rows k, v
+ * [total, heads_kv, 128] bf16) goes to position start[b] + i (device int32 [batch], >= 0).
+ * e4m3 pages: every row of 128 gets its own scale, the least power of two that brings
+ * its largest finite magnitude to 448 or below (scale within [9, 246]), and its values are
+ * rounded to the nearest e4m3 (ties to even; infinities become the largest, NaN stays).
+ * A sequence whose tokens do not fit is not written at all; a token whose page is out of
+ * range is not written.  Sequences that write must not share the pages that they write
+ * (no order is kept between two writes of one position).
+ */
+stree_status stree_cache_write(const void *k, const void *v, const int32_t *cu_seqlens, const int32_t *start,
+                               const int32_t *page_table, int total, int batch, int heads_kv, int head_dim,
+                               int n_pages, int page_size, int max_pages, stree_dtype dtype, stree_dtype cache_dtype,
+                               void *k_pages, void *v_pages, uint8_t *k_scales, uint8_t *v_scales, int32_t *err_out,
+                               void *stream);
+
+/*
+ * The same for the accepted path of a verified tree (what stree_commit is to a state):
+ * node accepted_path[b][i] of k_tree, v_tree [batch, n_nodes, heads_kv, 128] goes to
+ * position start[b] + i, i < path_len[b] (clamped to [0, maxlen]).  A node outside
+ * [0, n_nodes) latches STREE_ERR_BAD_PATH and is not written.  n_nodes and maxlen up to 256.
+ */
+stree_status stree_cache_commit(const void *k_tree, const void *v_tree, const int32_t *accepted_path,
+                                const int32_t *path_len, int maxlen, const int32_t *start, const int32_t *page_table,
+                                int n_nodes, int batch, int heads_kv, int head_dim, int n_pages, int page_size,
+                                int max_pages, stree_dtype dtype, stree_dtype cache_dtype, void *k_pages,
+                                void *v_pages, uint8_t *k_scales, uint8_t *v_scales, int32_t *err_out, void *stream);
+
+/*
+ * Reads pages back into the contiguous cache of stree_tree_attention: positions
+ * j < seq_len[b] (clamped to [0, ctx_cap]) of k_ctx, v_ctx [batch, ctx_cap, heads_kv, 128]
+ * bf16; later positions are left as they were, and so is a position whose page is out
+ * of range.  Exact: every e4m3 value times its scale (within [9, 246]) is a bf16.
+ */
+stree_status stree_cache_read(const void *k_pages, const void *v_pages, const uint8_t *k_scales,
+                              const uint8_t *v_scales, const int32_t *page_table, const int32_t *seq_len, int batch,
+                              int ctx_cap, int heads_kv, int head_dim, int n_pages, int page_size, int max_pages,
+                              stree_dtype cache_dtype, stree_dtype dtype, void *k_ctx, void *v_ctx, int32_t *err_out,
+                              void *stream);
 
 /*
  * Resolve accepted paths against the context's current tree: leaf_out[b] (device
