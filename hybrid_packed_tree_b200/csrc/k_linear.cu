@@ -301,7 +301,8 @@ extern "C" stree_status stree_linear_prompt_workspace_size(int batch, int total,
     if (!bytes) return STREE_ERR_INVALID_ARG;
     if (!shape_ok(batch, heads_v, heads_k, dk, dv, dtype) || total < 0) return STREE_ERR_UNSUPPORTED;
     *bytes = 0;
-    return STREE_OK;
+    if (batch == 0 || !linear_tc_supported(heads_v, heads_k, dk, dv, dtype)) return STREE_OK;
+    return linear_tc_workspace(batch, total, heads_v, dv, bytes) == cudaSuccess ? STREE_OK : STREE_ERR_CUDA;
 }
 
 extern "C" stree_status stree_linear_prompt(const void *q, const void *k, const void *v, const float *alpha,
@@ -321,6 +322,8 @@ extern "C" stree_status stree_linear_prompt(const void *q, const void *k, const 
     if (st != STREE_OK) return st;
     if (workspace && !aligned(workspace, 16)) return STREE_ERR_MISALIGNED;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (linear_tc_supported(heads_v, heads_k, dk, dv, dtype))
+        return launch_linear_tc(a, workspace, workspace_bytes, s) == cudaSuccess ? STREE_OK : STREE_ERR_CUDA;
     if (err_out && launch_pdl(linear_check_kernel, dim3(1), kThreads, 0, s, a) != cudaSuccess) return STREE_ERR_CUDA;
     const cudaError_t e = dtype == STREE_BF16 ? launch_prompt<__nv_bfloat16>(a, s) : launch_prompt<float>(a, s);
     return e == cudaSuccess ? STREE_OK : STREE_ERR_CUDA;

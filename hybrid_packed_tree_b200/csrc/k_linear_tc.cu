@@ -1,0 +1,668 @@
+// k_linear_tc.cu -- linear attention with a decay for each head over whole prompts, in
+// chunks of 128 tokens on the tensor cores (bf16, dk = 128, dv = 128 or 64), sm_100a.
+//
+// With L_t the sum of log2 alpha over the chunk up to token t, C its last token and S the
+// state before the chunk:
+//   P_ij = 2^(L_i - L_j) beta_j (q_i . k_j) for j <= i (+ skip where j = i), 0 beyond
+//   O    = P V + diag(2^L) Q S^T
+//   S'   = 2^L_C S + sum_j (w_j v_j) k_j^T,  w_j = 2^(L_C - L_j) beta_j
+// four 128 x 128 x 128 products a chunk.  No exponent above is positive for alpha <= 1.
+//
+// A CTA walks the chunks of one sequence and 128 value columns (one head of 128, or two of 64 that
+// share keys and queries: their Q K^T is one product).  Few sequences of many tokens are
+// cut into segments: a first launch takes every segment but the last from a zero state and
+// leaves its state and log decay in the workspace, and the walk of a segment starts from S0
+// folded with its predecessors' (the recurrence is linear).  The first launch also copies S0,
+// which the last segment may overwrite while others start from it.
+//
+// Precision.  P and the copy of S that Q multiplies are rounded to bf16 (they only enter o,
+// itself bf16).  The state is kept in fp32 registers and receives w_j v_j as three bf16 parts
+// (24 bits), so its products are those of fp32; L is summed in 64 bits, and every exponent
+// is a difference of L's taken before it is rounded.
+//
+// Warp roles (16 warps, bounded mbarrier waits): a producer (TMA: K, Q, V tiles of 32 KB into a
+// ring of five), the MMA issuer, a gate warp (L, w and the factors of P, one chunk ahead),
+// four warps for P and O (a token per thread), and eight for the state (a row of S per
+// thread and half of its columns): they read V by columns and put the three parts of w v into tensor
+// memory as the A operand, 32 tokens at a time in two alternating buffers, then add the product
+// to their registers and write the bf16 copy of S for the next chunk's Q S^T.
+//
+// P below the diagonal 32 x 32 blocks is a product of a row factor 2^(L_i - L_J) and a column
+// factor 2^(L_J - L_j) beta_j, J the last token of j's block: both at most 1, and one exponential per
+// row and block instead of one per pair.
+#include <cuda.h>
+
+#include <mutex>
+
+#include "linear.cuh"
+#include "seq_pages.cuh"
+#include "tc_ptx.cuh"
+#include "tmap.cuh"
+
+namespace stree {
+namespace {
+
+constexpr int kC = 128;                        // tokens per chunk; also dk and the value columns of a CTA
+constexpr int kThreads = 512;
+constexpr int kSlots = 5;
+constexpr uint32_t kTile = 128 * 128 * 2, kHalf = kTile / 2;
+constexpr float kLogZero = -130.f;             // log2 of a decay of zero: 2^-130 is flushed to zero
+constexpr int kMaxSegments = 8;
+constexpr int kMaxDevices = 64;
+
+enum Bars {
+    B_F = 0, B_E = B_F + kSlots, B_GF = B_E + kSlots, B_GE = B_GF + 2, B_SF = B_GE + 2, B_PF, B_OQ, B_OF, B_OE, B_SOP,
+    B_WF, B_WE = B_WF + 2, B_DF = B_WE + 2, B_DRAIN, kBars
+};
+
+// Tensor memory: Q K^T, then P over it (64 columns a head); O; the state's update; the parts of w v.
+constexpr uint32_t kColP = 0, kColO = 128, kColD = 256, kColW = 384;
+
+struct Gates {                                 // of one chunk, per head
+    float rel[2][kC];                          // L_i less L at the end of the block before i's
+    float beta[2][kC];
+    float fac[2][kC];                          // 2^(L at the end of j's block - L_j) beta_j
+    float w[2][kC];
+    double end[2][4];                          // L at the end of each 32-token block
+};
+
+struct TcArgs {
+    const float *alpha, *beta, *skip, *S0;
+    const int32_t *cu;
+    __nv_bfloat16 *o;
+    float *S_new;
+    float *seg_state;                          // [item][segments][128][128]: S0, then every segment's but the last
+    double *seg_log;                           // [item][segments - 1][2]
+    int32_t *err;
+    int total, batch, heads_v, heads_k, per_seq, segments;   // per_seq: 128-column items of a sequence
+};
+
+constexpr uint32_t kSmem = kSlots * kTile + kTile + 2 * sizeof(Gates) + 1024;
+
+// Rows [valid, 128) of a tile of tokens become zero (they belong to another sequence).
+__device__ __forceinline__ void zero_rows(uint8_t *tile, int valid, int lane)
+{
+    for (int e = lane; e < (kC - valid) * 16; e += 32) {
+        const int r = valid + e / 16, c = e % 16;
+        *reinterpret_cast<uint4 *>(tile + (c >> 3) * kHalf + r * 128 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// NH: heads in the CTA's 128 value columns.  kState: the first launch of a split (state only).
+template <int NH, bool kState>
+__global__ void __launch_bounds__(kThreads, 1)
+linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                 const __grid_constant__ CUtensorMap tm_v, const TcArgs a)
+{
+    constexpr int kDv = kC / NH;
+    constexpr int kLoads = kState ? 2 : 3;     // tiles per chunk: K, (Q,) V
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    __shared__ uint64_t bars[kBars];
+    __shared__ volatile int aborted;
+    __shared__ uint32_t tmem_s;
+    uint8_t *smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint8_t *sop = smem + kSlots * kTile;      // the bf16 state, K-major
+    Gates *gates = reinterpret_cast<Gates *>(sop + kTile);
+    auto bar = [&](int i) { return ptx::smem_u32(&bars[i]); };
+    const uint32_t ring = ptx::smem_u32(smem), sop_u = ptx::smem_u32(sop);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    pdl_start();
+    if (!kState && blockIdx.x == gridDim.x - 1) {   // the error word
+        PageCheck c{};
+        c.cu = a.cu;
+        c.batch = a.batch;
+        c.total = a.total;
+        check_pages(c, a.err);
+        return;
+    }
+    const int segs = kState ? a.segments - 1 : a.segments;
+    const int seg = blockIdx.x % segs, flat = blockIdx.x / segs;   // flat: (sequence, 128-column item)
+    const int item = flat % a.per_seq, b = flat / a.per_seq;
+    const int head0 = item * NH, g = head0 / (a.heads_v / a.heads_k);
+    const int2 seq = seq_range(a.cu, b, a.total);
+    const int len = seq.y - seq.x, chunks = (len + kC - 1) / kC;
+    const int c0 = (int)((long long)chunks * seg / a.segments), n = (int)((long long)chunks * (seg + 1) / a.segments) - c0;
+    const bool last = seg == a.segments - 1;
+    if (n == 0 && !kState && !last) return;    // nothing to put out
+
+    auto wait = [&](int i, uint32_t parity, int where) -> bool {
+        if (aborted) return false;
+        if (ptx::mbar_wait(bar(i), parity & 1)) return true;
+        if (a.err) latch_error(a.err, STREE_ERR_TIMEOUT, b, where, (int)parity);
+        aborted = 1;
+        return false;
+    };
+    // One lane waits for the warp.
+    auto warp_wait = [&](int i, uint32_t parity, int where) -> bool {
+        bool r = true;
+        if (lane == 0) r = wait(i, parity, where);
+        return __shfl_sync(0xffffffffu, r ? 1 : 0, 0) != 0;
+    };
+    if (tid == 0) {
+        ptx::prefetch_tensormap(&tm_q);
+        ptx::prefetch_tensormap(&tm_k);
+        ptx::prefetch_tensormap(&tm_v);
+        for (int i = 0; i < kBars; ++i) {
+            const int count = i == B_PF || i == B_OE || i == B_WF || i == B_WF + 1 ? 4
+                              : i == B_SOP                                         ? 8
+                              : i == B_GE || i == B_GE + 1                         ? (kState ? 8 : 12)
+                                                                                   : 1;
+            ptx::mbar_init(bar(i), count);
+        }
+        ptx::fence_mbar_init();
+        aborted = 0;
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(ptx::smem_u32(&tmem_s), 512);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = tmem_s;
+    // Load numbers of a chunk: K, then Q, then V.
+    auto load_k = [&](int i) { return kLoads * i; };
+    auto load_q = [&](int i) { return kLoads * i + 1; };
+    auto load_v = [&](int i) { return kLoads * i + kLoads - 1; };
+
+    int loads = 0;
+    if (warp < 4) {
+        if (warp == 0 && lane == 0) {
+            // ------------------------------------------------------------ producer
+            for (; loads < kLoads * n; ++loads) {
+                const int s = loads % kSlots, i = loads / kLoads, what = loads % kLoads;
+                if (loads >= kSlots && !wait(B_E + s, (uint32_t)(loads / kSlots - 1), 1)) break;
+                const bool is_v = what == kLoads - 1;
+                const CUtensorMap *m = is_v ? &tm_v : what == 0 ? &tm_k : &tm_q;
+                ptx::mbar_expect_tx(bar(B_F + s), kTile);
+                for (int hh = 0; hh < 2; ++hh)
+                    ptx::tma_load_3d(ring + s * kTile + hh * kHalf, m, hh * 64, is_v ? item : g, seq.x + (c0 + i) * kC, bar(B_F + s));
+            }
+        } else if (warp == 1) {
+            // ------------------------------------------------------------ MMA issue
+            const uint32_t id_kk = ptx::idesc_bf16_kk(kC, kC), id_mn = ptx::idesc_bf16_bmn(kC, kC),
+                           id_pv = ptx::idesc_bf16_bmn(kC, kDv);
+            auto arrived = [&](int x, int where) { return warp_wait(B_F + x % kSlots, (uint32_t)(x / kSlots), where); };
+            auto slot = [&](int x) { return ring + (x % kSlots) * kTile; };
+            auto release = [&](int x) {        // a slot that another load will use
+                if (x + kSlots < kLoads * n) ptx::mma_commit(bar(B_E + x % kSlots));
+            };
+            bool ok = true;
+            for (int i = 0; i < n && ok; ++i) {
+                const int valid = min(kC, len - (c0 + i) * kC);
+                const uint32_t k0 = slot(load_k(i)), q0 = slot(load_q(i)), v0 = slot(load_v(i));
+                if (!(ok = arrived(load_k(i), 10))) break;
+                if (valid < kC) zero_rows(smem + (load_k(i) % kSlots) * kTile, valid, lane);
+                if (!kState) {
+                    if (!(ok = arrived(load_q(i), 11))) break;
+                    if (lane == 0) {
+                        ptx::tc_fence_after();
+#pragma unroll
+                        for (int kk = 0; kk < kC / 16; ++kk)
+                            ptx::mma_f16(tmem + kColP, ptx::desc_kmajor_sw128(q0 + (kk >> 2) * kHalf + (kk & 3) * 32),
+                                         ptx::desc_kmajor_sw128(k0 + (kk >> 2) * kHalf + (kk & 3) * 32), id_kk, kk != 0);
+                        ptx::mma_commit(bar(B_SF));
+                    }
+                    __syncwarp();
+                    // Q S^T, once the state's copy is there and the last chunk's O has been read.
+                    if (!(ok = warp_wait(B_SOP, (uint32_t)i, 12)) || (i > 0 && !(ok = warp_wait(B_OE, (uint32_t)(i - 1), 13)))) break;
+                    if (lane == 0) {
+                        ptx::tc_fence_after();
+#pragma unroll
+                        for (int kk = 0; kk < kC / 16; ++kk)
+                            ptx::mma_f16(tmem + kColO, ptx::desc_kmajor_sw128(q0 + (kk >> 2) * kHalf + (kk & 3) * 32),
+                                         ptx::desc_kmajor_sw128(sop_u + (kk >> 2) * kHalf + (kk & 3) * 32), id_kk, kk != 0);
+                        ptx::mma_commit(bar(B_OQ));
+                        release(load_q(i));
+                    }
+                    __syncwarp();
+                } else if (i > 0 && !(ok = warp_wait(B_SOP, (uint32_t)(i - 1), 12))) {
+                    break;                     // the last update has been read
+                }
+                // The state's update: 32 tokens at a time, three parts of two steps each.
+                for (int s = 0; s < 4 && ok; ++s) {
+                    if (!(ok = warp_wait(B_WF + (s & 1), (uint32_t)(2 * i + (s >> 1)), 14))) break;
+                    if (lane == 0) {
+                        ptx::tc_fence_after();
+#pragma unroll
+                        for (int part = 0; part < 3; ++part)
+#pragma unroll
+                            for (int kk = 0; kk < 2; ++kk)
+                                ptx::mma_f16_ta(tmem + kColD, tmem + kColW + (s & 1) * 64 + part * 16 + kk * 8,
+                                                ptx::desc_mnmajor_sw128(k0 + (2 * s + kk) * 2048, kHalf, 1024), id_mn,
+                                                (s | part | kk) != 0);
+                        ptx::mma_commit(bar(B_WE + (s & 1)));
+                    }
+                    __syncwarp();
+                }
+                if (!ok) break;
+                if (lane == 0) {
+                    ptx::mma_commit(bar(B_DF));
+                    release(load_k(i));
+                }
+                __syncwarp();
+                if (kState) {
+                    // The state warps have read V before they handed over its last part.
+                    if (lane == 0) release(load_v(i));
+                    __syncwarp();
+                    continue;
+                }
+                if (!(ok = arrived(load_v(i), 15))) break;
+                if (valid < kC) zero_rows(smem + (load_v(i) % kSlots) * kTile, valid, lane);
+                if (!(ok = warp_wait(B_PF, (uint32_t)i, 16))) break;
+                if (lane == 0) {
+                    ptx::tc_fence_after();
+#pragma unroll
+                    for (int hh = 0; hh < NH; ++hh)
+#pragma unroll
+                        for (int kk = 0; kk < kC / 16; ++kk)
+                            ptx::mma_f16_ta(tmem + kColO + hh * kDv, tmem + kColP + hh * 64 + kk * 8,
+                                            ptx::desc_mnmajor_sw128(v0 + hh * kHalf + kk * 2048, kHalf, 1024), id_pv, 1);
+                    ptx::mma_commit(bar(B_OF));
+                    release(load_v(i));
+                }
+                __syncwarp();
+            }
+        } else if (warp == 2) {
+            // ------------------------------------------------------------ gates
+            double total[2] = {0.0, 0.0};
+            float al[NH][4], be[NH][4];
+            auto fetch = [&](int i) {          // four tokens a lane
+#pragma unroll
+                for (int h = 0; h < NH; ++h)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int t = (c0 + i) * kC + lane * 4 + e;
+                        const size_t at = (size_t)(seq.x + t) * a.heads_v + head0 + h;
+                        al[h][e] = t < len ? __ldg(a.alpha + at) : 1.f;
+                        be[h][e] = t < len ? (a.beta ? __ldg(a.beta + at) : 1.f) : 0.f;   // weight zero past the end
+                    }
+            };
+            if (n > 0) fetch(0);
+            for (int i = 0; i < n; ++i) {
+                if (i >= 2 && !warp_wait(B_GE + (i & 1), (uint32_t)((i >> 1) - 1), 30)) break;
+                Gates &G = gates[i & 1];
+#pragma unroll
+                for (int h = 0; h < NH; ++h) {
+                    double L[4], sum = 0.0;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float lg = log2f(al[h][e]);
+                        lg = lg < kLogZero ? kLogZero : lg;
+                        sum += (double)lg;
+                        L[e] = sum;
+                    }
+                    double scan = sum;
+#pragma unroll
+                    for (int d = 1; d < 32; d <<= 1) {
+                        const double u = __shfl_up_sync(0xffffffffu, scan, d);
+                        if (lane >= d) scan += u;
+                    }
+                    const double before = scan - sum;
+                    // Eight lanes are a block: its end, and the end of the block before it.
+                    const double blk_end = __shfl_sync(0xffffffffu, scan, lane | 7);
+                    const double prev = __shfl_sync(0xffffffffu, scan, max((lane & 24) - 1, 0));
+                    const double blk_start = lane < 8 ? 0.0 : prev, all = __shfl_sync(0xffffffffu, scan, 31);
+                    if ((lane & 7) == 7) G.end[h][lane >> 3] = scan;
+                    float4 rel, fac, w;
+                    float *rp = &rel.x, *fp = &fac.x, *wp = &w.x;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const double Le = before + L[e];
+                        rp[e] = (float)(Le - blk_start);
+                        fp[e] = exp2f((float)(blk_end - Le)) * be[h][e];
+                        wp[e] = exp2f((float)(all - Le)) * be[h][e];
+                    }
+                    *reinterpret_cast<float4 *>(&G.rel[h][lane * 4]) = rel;
+                    *reinterpret_cast<float4 *>(&G.fac[h][lane * 4]) = fac;
+                    *reinterpret_cast<float4 *>(&G.w[h][lane * 4]) = w;
+                    *reinterpret_cast<float4 *>(&G.beta[h][lane * 4]) = make_float4(be[h][0], be[h][1], be[h][2], be[h][3]);
+                    total[h] += all;
+                }
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar(B_GF + (i & 1)));
+                if (i + 1 < n) fetch(i + 1);
+            }
+            if (kState && lane < NH) a.seg_log[((size_t)flat * segs + seg) * 2 + lane] = lane == 0 ? total[0] : total[1];
+        }
+    } else if (warp < 8) {
+        // ---------------------------------------------------------------- P and O
+        if (!kState) {
+            const int quad = warp & 3, r = quad * 32 + lane;
+            const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+            const uint32_t t_p = tmem + kColP + lanes, t_o = tmem + kColO + lanes;
+            float skip[NH];
+#pragma unroll
+            for (int h = 0; h < NH; ++h) skip[h] = a.skip ? __ldg(a.skip + head0 + h) : 0.f;
+            for (int i = 0; i < n; ++i) {
+                const Gates &G = gates[i & 1];
+                if (!warp_wait(B_GF + (i & 1), (uint32_t)(i >> 1), 20) || !warp_wait(B_SF, (uint32_t)i, 21)) break;
+                ptx::tc_fence_after();
+                // With two heads the second one's P lies over the scores' upper half: those are held in
+                // registers (rows that see them) before anything is written.
+                uint32_t held[NH == 2 ? 2 : 1][32];
+                if (NH == 2 && quad >= 2) {
+                    ptx::tmem_ld32(t_p + 64, held[0]);
+                    if (quad == 3) ptx::tmem_ld32(t_p + 96, held[NH - 1]);
+                }
+                float rel[NH], gamma[NH];
+                double start[NH];
+#pragma unroll
+                for (int h = 0; h < NH; ++h) {
+                    rel[h] = G.rel[h][r];
+                    start[h] = quad == 0 ? 0.0 : G.end[h][quad - 1];
+                    gamma[h] = ptx::ex2_approx((float)start[h] + rel[h]);
+                }
+#pragma unroll
+                for (int J = 0; J < 4; ++J) {
+                    uint32_t now[32];
+                    const uint32_t(&sv)[32] = NH == 2 && J >= 2 ? held[J - 2] : now;
+                    if ((NH == 1 || J < 2) && J <= quad) ptx::tmem_ld32(t_p + J * 32, now);
+#pragma unroll
+                    for (int h = 0; h < NH; ++h) {
+                        uint32_t pk[16];
+                        if (J < quad) {
+                            const float row = ptx::ex2_approx((float)(start[h] - G.end[h][J]) + rel[h]);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const float4 f = *reinterpret_cast<const float4 *>(&G.fac[h][J * 32 + 4 * e]);
+                                const uint32_t *x = &sv[4 * e];
+                                pk[2 * e] = pack2(__uint_as_float(x[0]) * (row * f.x), __uint_as_float(x[1]) * (row * f.y));
+                                pk[2 * e + 1] = pack2(__uint_as_float(x[2]) * (row * f.z), __uint_as_float(x[3]) * (row * f.w));
+                            }
+                        } else if (J == quad) {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                float p[2];
+#pragma unroll
+                                for (int u = 0; u < 2; ++u) {
+                                    const int j = 2 * e + u;
+                                    const float f = ptx::ex2_approx(rel[h] - G.rel[h][J * 32 + j]) * G.beta[h][J * 32 + j];
+                                    p[u] = j <= lane ? __uint_as_float(sv[j]) * f : 0.f;
+                                    if (j == lane) p[u] += skip[h];
+                                }
+                                pk[e] = pack2(p[0], p[1]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) pk[e] = 0u;
+                        }
+                        ptx::tmem_st16(t_p + h * 64 + J * 16, pk);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar(B_GE + (i & 1)));
+                if (!warp_wait(B_OQ, (uint32_t)i, 22)) break;
+                ptx::tc_fence_after();
+                // diag(2^L) Q S^T, onto which P V is added.
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t ov[32];
+                    ptx::tmem_ld32(t_o + c * 32, ov);
+                    const float gm = gamma[NH == 2 ? c >> 1 : 0];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(gm * __uint_as_float(ov[e]));
+                    ptx::tmem_st32(t_o + c * 32, ov);
+                }
+                ptx::tmem_wait_st();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar(B_PF));   // P written, Q S^T scaled
+                if (!warp_wait(B_OF, (uint32_t)i, 23)) break;
+                ptx::tc_fence_after();
+                const int t = (c0 + i) * kC + r;
+                __nv_bfloat16 *row = a.o + ((size_t)(seq.x + t) * a.per_seq + item) * kC;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t ov[32];
+                    ptx::tmem_ld32(t_o + c * 32, ov);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            w[u] = pack2(__uint_as_float(ov[8 * e + 2 * u]), __uint_as_float(ov[8 * e + 2 * u + 1]));
+                        if (t < len) *reinterpret_cast<uint4 *>(row + c * 32 + 8 * e) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar(B_OE));
+            }
+        }
+    } else {
+        // ---------------------------------------------------------------- the state
+        const int wg = (warp >> 2) - 2, quad = warp & 3, r = quad * 32 + lane;   // row r of S, columns 64 wg ..
+        const int h = NH == 2 ? r / kDv : 0;
+        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+        const size_t at = ((size_t)flat * kC + r) * kC + wg * 64;   // [batch, heads_v, dv] rows are flat 128-row items
+        float st[64];
+        // S0, by way of the workspace when segments start from it while the last one writes S_new.
+        float *const slots = a.segments > 1 ? a.seg_state + ((size_t)flat * a.segments * kC + r) * kC + wg * 64 : nullptr;
+        const float *from = !a.S0 ? nullptr : !kState && a.segments > 1 ? slots : a.S0 + at;
+        if (kState && (seg > 0 || !a.S0)) from = nullptr;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            float4 x = from ? reinterpret_cast<const float4 *>(from)[e] : make_float4(0.f, 0.f, 0.f, 0.f);
+            if (kState && from) {              // segment 0 copies it; its own state is taken from zero
+                reinterpret_cast<float4 *>(slots)[e] = x;
+                x = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            st[4 * e] = x.x;
+            st[4 * e + 1] = x.y;
+            st[4 * e + 2] = x.z;
+            st[4 * e + 3] = x.w;
+        }
+        if (!kState)
+            for (int s = 0; s < seg; ++s) {    // the segments before this one
+                const size_t p = (size_t)flat * (a.segments - 1) + s;
+                const float f = exp2f((float)a.seg_log[p * 2 + h]);
+                const float4 *src = reinterpret_cast<const float4 *>(slots + (size_t)(s + 1) * kC * kC);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float4 x = src[e];
+                    st[4 * e] = fmaf(f, st[4 * e], x.x);
+                    st[4 * e + 1] = fmaf(f, st[4 * e + 1], x.y);
+                    st[4 * e + 2] = fmaf(f, st[4 * e + 2], x.z);
+                    st[4 * e + 3] = fmaf(f, st[4 * e + 3], x.w);
+                }
+            }
+        // The bf16 copy that the next Q S^T reads: row r of this half.
+        auto copy_out = [&] {
+            if (!kState) {
+                uint8_t *dst = sop + wg * kHalf + r * 128;
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    *reinterpret_cast<uint4 *>(dst + ((c ^ (r & 7)) << 4)) =
+                        make_uint4(pack2(st[8 * c], st[8 * c + 1]), pack2(st[8 * c + 2], st[8 * c + 3]),
+                                   pack2(st[8 * c + 4], st[8 * c + 5]), pack2(st[8 * c + 6], st[8 * c + 7]));
+                ptx::fence_proxy_async_smem();
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar(B_SOP));
+        };
+        if (!kState && n > 0) copy_out();
+        bool run = true;
+        for (int i = 0; i < n; ++i) {
+            const Gates &G = gates[i & 1];
+            const int x = load_v(i), valid = min(kC, len - (c0 + i) * kC);
+            if (!(run = warp_wait(B_GF + (i & 1), (uint32_t)(i >> 1), 40) && warp_wait(B_F + x % kSlots, (uint32_t)(x / kSlots), 41))) break;
+            const uint8_t *v = smem + (x % kSlots) * kTile + (r >> 6) * kHalf + (r & 7) * 2;
+            const int chunk = (r & 63) >> 3;
+            for (int u = 0; u < 2 && run; ++u) {
+                const int s = 2 * u + wg, uses = 2 * i + u;
+                if (uses > 0 && !(run = warp_wait(B_WE + wg, (uint32_t)(uses - 1), 42))) break;
+                ptx::tc_fence_after();
+                uint32_t p0[16], p1[16], p2[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    float y[2];
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+                        const int t = s * 32 + 2 * e + z;
+                        const uint16_t bits = *reinterpret_cast<const uint16_t *>(v + t * 128 + ((chunk ^ (t & 7)) << 4));
+                        y[z] = t < valid ? G.w[h][t] * __uint_as_float((uint32_t)bits << 16) : 0.f;
+                    }
+                    p0[e] = pack2(y[0], y[1]);
+                    const float a0 = y[0] - low(p0[e]), a1 = y[1] - high(p0[e]);
+                    p1[e] = pack2(a0, a1);
+                    p2[e] = pack2(a0 - low(p1[e]), a1 - high(p1[e]));
+                }
+                const uint32_t t_w = tmem + kColW + wg * 64 + lanes;
+                ptx::tmem_st16(t_w, p0);
+                ptx::tmem_st16(t_w + 16, p1);
+                ptx::tmem_st16(t_w + 32, p2);
+                ptx::tmem_wait_st();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar(B_WF + wg));
+            }
+            if (!run) break;
+            const float decay = exp2f((float)G.end[h][3]);
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar(B_GE + (i & 1)));
+            if (!(run = warp_wait(B_DF, (uint32_t)i, 43))) break;
+            ptx::tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t d[32];
+                ptx::tmem_ld32(tmem + kColD + wg * 64 + c * 32 + lanes, d);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) st[c * 32 + e] = fmaf(decay, st[c * 32 + e], __uint_as_float(d[e]));
+            }
+            if (i + 1 < n) copy_out();         // Q S^T of this chunk was issued before its update and is done
+        }
+        float *dst = kState ? slots + (size_t)(seg + 1) * kC * kC
+                            : last && a.S_new ? a.S_new + at : nullptr;
+        if (dst && run)
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                reinterpret_cast<float4 *>(dst)[e] = make_float4(st[4 * e], st[4 * e + 1], st[4 * e + 2], st[4 * e + 3]);
+    }
+
+    // -------------------------------------------------------------------- teardown
+    if (warp == 1 && lane == 0 && aborted) {
+        ptx::mma_commit(bar(B_DRAIN));         // every issued MMA completes first
+        ptx::mbar_wait(bar(B_DRAIN), 0);
+    }
+    if (warp == 0 && lane == 0 && aborted)
+        for (int x = max(0, loads - kSlots); x < loads; ++x) ptx::mbar_wait(bar(B_F + x % kSlots), (uint32_t)((x / kSlots) & 1));
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, 512);
+    }
+}
+
+std::mutex g_mutex;
+int g_sms[kMaxDevices] = {};
+
+cudaError_t prepare(int *sms)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(g_mutex);
+    if (!g_sms[dev]) {
+        const auto set = [](auto *f) { return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem); };
+        if ((e = set(linear_tc_kernel<1, false>)) != cudaSuccess || (e = set(linear_tc_kernel<2, false>)) != cudaSuccess ||
+            (e = set(linear_tc_kernel<1, true>)) != cudaSuccess || (e = set(linear_tc_kernel<2, true>)) != cudaSuccess)
+            return e;
+        int n = 0;
+        if ((e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+        g_sms[dev] = n > 0 ? n : 1;
+    }
+    *sms = g_sms[dev];
+    return cudaSuccess;
+}
+
+// Segments of a sequence: as many as fill the SMs with one CTA each, while a segment of a
+// sequence of average length has at least four chunks (a CTA's set-up and the first launch
+// cost about two).
+int segments_for(int batch, int total, int items, int sms)
+{
+    int s = sms / (items > 0 ? items : 1);
+    const int by_len = total / (batch > 0 ? batch : 1) / (4 * kC);
+    s = s < by_len ? s : by_len;
+    return s < 1 ? 1 : s > kMaxSegments ? kMaxSegments : s;
+}
+
+size_t workspace_for(int items, int segments)
+{
+    return segments > 1 ? (size_t)items * segments * (kC * kC * sizeof(float) + 2 * sizeof(double)) : 0;
+}
+
+}  // namespace
+
+bool linear_tc_supported(int heads_v, int heads_k, int dk, int dv, stree_dtype dtype)
+{
+    return dtype == STREE_BF16 && dk == kC && (dv == kC || (dv == kC / 2 && (heads_v / heads_k) % 2 == 0));
+}
+
+cudaError_t linear_tc_workspace(int batch, int total, int heads_v, int dv, size_t *bytes)
+{
+    int sms = 0;
+    const cudaError_t e = prepare(&sms);
+    if (e != cudaSuccess) return e;
+    const int items = batch * (heads_v * dv / kC);
+    *bytes = workspace_for(items, segments_for(batch, total, items, sms));
+    return cudaSuccess;
+}
+
+cudaError_t launch_linear_tc(const LinearArgs &l, void *workspace, size_t workspace_bytes, cudaStream_t s)
+{
+    int sms = 0;
+    cudaError_t e = prepare(&sms);
+    if (e != cudaSuccess) return e;
+    TcArgs a{};
+    a.alpha = l.alpha;
+    a.beta = l.beta;
+    a.skip = l.skip;
+    a.S0 = l.S0;
+    a.cu = l.cu;
+    a.o = static_cast<__nv_bfloat16 *>(l.o);
+    a.S_new = l.S_new;
+    a.err = l.err;
+    a.total = l.total;
+    a.batch = l.batch;
+    a.heads_v = l.heads_v;
+    a.heads_k = l.heads_k;
+    a.per_seq = l.heads_v * l.dv / kC;
+    const int items = l.batch * a.per_seq;
+    a.segments = segments_for(l.batch, l.total, items, sms);
+    if (!workspace || workspace_bytes < workspace_for(items, a.segments)) a.segments = 1;
+    if (a.segments > 1) {
+        a.seg_log = static_cast<double *>(workspace);
+        a.seg_state = reinterpret_cast<float *>(a.seg_log + (size_t)items * a.segments * 2);
+    }
+    CUtensorMap q{}, k{}, v{};
+    if (l.total > 0 && (!encode_heads(&q, l.q, l.total, l.heads_k, 1, kC) || !encode_heads(&k, l.k, l.total, l.heads_k, 1, kC) ||
+                        !encode_heads(&v, l.v, l.total, a.per_seq, 1, kC)))
+        return cudaErrorInvalidValue;
+    const bool one = l.dv == kC;
+    if (a.segments > 1) {
+        const dim3 grid((unsigned)(items * (a.segments - 1)));
+        e = one ? launch_pdl(linear_tc_kernel<1, true>, grid, kThreads, kSmem, s, q, k, v, a)
+                : launch_pdl(linear_tc_kernel<2, true>, grid, kThreads, kSmem, s, q, k, v, a);
+        if (e != cudaSuccess) return e;
+    }
+    const dim3 grid((unsigned)(items * a.segments + 1));
+    return one ? launch_pdl(linear_tc_kernel<1, false>, grid, kThreads, kSmem, s, q, k, v, a)
+               : launch_pdl(linear_tc_kernel<2, false>, grid, kThreads, kSmem, s, q, k, v, a);
+}
+
+}  // namespace stree

@@ -17,4 +17,10 @@ struct LinearArgs {
     stree_dtype dtype;
 };
 
+// The tensor-core prompt pass: whether it takes the shape, the workspace in which it
+// splits long sequences over CTAs, and the launch (one CTA per item without enough of it).
+bool linear_tc_supported(int heads_v, int heads_k, int dk, int dv, stree_dtype dtype);
+cudaError_t linear_tc_workspace(int batch, int total, int heads_v, int dv, size_t *bytes);
+cudaError_t launch_linear_tc(const LinearArgs &a, void *workspace, size_t workspace_bytes, cudaStream_t s);
+
 }  // namespace stree

@@ -443,7 +443,7 @@ stree_status stree_tree_attention_workspace_size(int n_nodes, int batch, int ctx
  * 128, or dv = 64 with an even number of value heads per key head, runs in chunks of 128
  * tokens on the tensor cores: the pair weights and the state that a chunk's queries
  * read are rounded to bf16 (they only enter o, itself bf16); the state itself is
- * accumulated in fp32 from products exact to 2^-17.
+ * accumulated in fp32 from fp32 products.
  */
 stree_status stree_linear_prompt(const void *q, const void *k, const void *v, const float *alpha, const float *beta,
                                  const float *skip, const float *S0, const int32_t *cu_seqlens, int total, int batch,

@@ -103,12 +103,16 @@ def test_prompt_without_the_optional_inputs(st, dv, skip, start, beta):
 
 @pytest.mark.parametrize("dv", [128, 64])
 def test_prompt_split_over_the_long_axis(st, dv):
-    a = _inputs([1100, 390], 2, 1, 128, dv, "bf16", seed=8, decay=np.array([1e-3, 0.02]))
+    lens = [2300, 1900, 5]
+    a = _inputs(lens, 2, 1, 128, dv, "bf16", seed=8, decay=np.array([1e-3, 0.02]))
+    assert st.stree_linear_prompt_workspace_size(len(lens), sum(lens), 2, 1, 128, dv) > 0
     whole = _run(st, a, split=False)
     split = _run(st, a, split=True)
     assert whole[2] == split[2] == [0, 0, 0, 0]
     _check(a, *whole[:2], "unsplit")
     _check(a, *split[:2], "split")
+    inp = _run(st, a, split=True, in_place=True)
+    assert torch.equal(inp[0], split[0]) and torch.equal(inp[1], split[1])
 
 
 @pytest.mark.parametrize("dtype,dv", [("bf16", 128), ("bf16", 64), ("f32", 64)])
