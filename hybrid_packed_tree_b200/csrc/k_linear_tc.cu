@@ -55,7 +55,8 @@ enum Bars {
     B_WF, B_WE = B_WF + 2, B_DF = B_WE + 2, B_DRAIN, kBars
 };
 
-// Tensor memory: Q K^T, then P over it (64 columns a head); O; the state's update; the parts of w v.
+// Tensor memory: Q K^T, then P over it (of every 32 columns, 16 for a head); O; the state's
+// update; the parts of w v.
 constexpr uint32_t kColP = 0, kColO = 128, kColD = 256, kColW = 384;
 
 struct Gates {                                 // of one chunk, per head
@@ -82,6 +83,7 @@ constexpr uint32_t kSmem = kSlots * kTile + kTile + 2 * sizeof(Gates) + 1024;
 // Rows [valid, 128) of a tile of tokens become zero (they belong to another sequence).
 __device__ __forceinline__ void zero_rows(uint8_t *tile, int valid, int lane)
 {
+#pragma unroll 1
     for (int e = lane; e < (kC - valid) * 16; e += 32) {
         const int r = valid + e / 16, c = e % 16;
         *reinterpret_cast<uint4 *>(tile + (c >> 3) * kHalf + r * 128 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
@@ -136,19 +138,9 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const bool last = seg == a.segments - 1;
     if (n == 0 && !kState && !last) return;    // nothing to put out
 
-    auto wait = [&](int i, uint32_t parity, int where) -> bool {
-        if (aborted) return false;
-        if (ptx::mbar_wait(bar(i), parity & 1)) return true;
-        if (a.err) latch_error(a.err, STREE_ERR_TIMEOUT, b, where, (int)parity);
-        aborted = 1;
-        return false;
-    };
-    // One lane waits for the warp.
-    auto warp_wait = [&](int i, uint32_t parity, int where) -> bool {
-        bool r = true;
-        if (lane == 0) r = wait(i, parity, where);
-        return __shfl_sync(0xffffffffu, r ? 1 : 0, 0) != 0;
-    };
+    const Waits waits{&aborted, a.err, b};
+    auto wait = [&](int i, uint32_t parity, int where) { return wait_one(waits, bar(i), parity, where); };
+    auto warp_wait = [&](int i, uint32_t parity, int where) { return wait_warp(waits, bar(i), parity, where); };
     if (tid == 0) {
         ptx::prefetch_tensormap(&tm_q);
         ptx::prefetch_tensormap(&tm_k);
@@ -231,6 +223,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     break;                     // the last update has been read
                 }
                 // The state's update: 32 tokens at a time, three parts of two steps each.
+#pragma unroll 1
                 for (int s = 0; s < 4 && ok; ++s) {
                     if (!(ok = warp_wait(B_WF + (s & 1), (uint32_t)(2 * i + (s >> 1)), 14))) break;
                     if (lane == 0) {
@@ -267,7 +260,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     for (int hh = 0; hh < NH; ++hh)
 #pragma unroll
                         for (int kk = 0; kk < kC / 16; ++kk)
-                            ptx::mma_f16_ta(tmem + kColO + hh * kDv, tmem + kColP + hh * 64 + kk * 8,
+                            ptx::mma_f16_ta(tmem + kColO + hh * kDv, tmem + kColP + (kk >> 1) * 32 + hh * 16 + (kk & 1) * 8,
                                             ptx::desc_mnmajor_sw128(v0 + hh * kHalf + kk * 2048, kHalf, 1024), id_pv, 1);
                     ptx::mma_commit(bar(B_OF));
                     release(load_v(i));
@@ -349,31 +342,17 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 const Gates &G = gates[i & 1];
                 if (!warp_wait(B_GF + (i & 1), (uint32_t)(i >> 1), 20) || !warp_wait(B_SF, (uint32_t)i, 21)) break;
                 ptx::tc_fence_after();
-                // With two heads the second one's P lies over the scores' upper half: those are held in
-                // registers (rows that see them) before anything is written.
-                uint32_t held[NH == 2 ? 2 : 1][32];
-                if (NH == 2 && quad >= 2) {
-                    ptx::tmem_ld32(t_p + 64, held[0]);
-                    if (quad == 3) ptx::tmem_ld32(t_p + 96, held[NH - 1]);
-                }
-                float rel[NH], gamma[NH];
-                double start[NH];
-#pragma unroll
-                for (int h = 0; h < NH; ++h) {
-                    rel[h] = G.rel[h][r];
-                    start[h] = quad == 0 ? 0.0 : G.end[h][quad - 1];
-                    gamma[h] = ptx::ex2_approx((float)start[h] + rel[h]);
-                }
-#pragma unroll
-                for (int J = 0; J < 4; ++J) {
-                    uint32_t now[32];
-                    const uint32_t(&sv)[32] = NH == 2 && J >= 2 ? held[J - 2] : now;
-                    if ((NH == 1 || J < 2) && J <= quad) ptx::tmem_ld32(t_p + J * 32, now);
+                float gamma[NH];
+#pragma unroll 1
+                for (int J = 0; J < 4; ++J) {  // 32 tokens j: read the scores, write P over them
+                    uint32_t sv[32];
+                    if (J <= quad) ptx::tmem_ld32(t_p + J * 32, sv);
 #pragma unroll
                     for (int h = 0; h < NH; ++h) {
                         uint32_t pk[16];
+                        const float rel = G.rel[h][r];
                         if (J < quad) {
-                            const float row = ptx::ex2_approx((float)(start[h] - G.end[h][J]) + rel[h]);
+                            const float row = ptx::ex2_approx((float)(G.end[h][quad - 1] - G.end[h][J]) + rel);
 #pragma unroll
                             for (int e = 0; e < 8; ++e) {
                                 const float4 f = *reinterpret_cast<const float4 *>(&G.fac[h][J * 32 + 4 * e]);
@@ -383,22 +362,26 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                             }
                         } else if (J == quad) {
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                float p[2];
+                            for (int e = 0; e < 8; ++e) {
+                                const float4 rj = *reinterpret_cast<const float4 *>(&G.rel[h][J * 32 + 4 * e]);
+                                const float4 bj = *reinterpret_cast<const float4 *>(&G.beta[h][J * 32 + 4 * e]);
+                                float p[4];
 #pragma unroll
-                                for (int u = 0; u < 2; ++u) {
-                                    const int j = 2 * e + u;
-                                    const float f = ptx::ex2_approx(rel[h] - G.rel[h][J * 32 + j]) * G.beta[h][J * 32 + j];
+                                for (int u = 0; u < 4; ++u) {
+                                    const int j = 4 * e + u;
+                                    const float f = ptx::ex2_approx(rel - (&rj.x)[u]) * (&bj.x)[u];
                                     p[u] = j <= lane ? __uint_as_float(sv[j]) * f : 0.f;
                                     if (j == lane) p[u] += skip[h];
                                 }
-                                pk[e] = pack2(p[0], p[1]);
+                                pk[2 * e] = pack2(p[0], p[1]);
+                                pk[2 * e + 1] = pack2(p[2], p[3]);
                             }
+                            gamma[h] = ptx::ex2_approx((quad == 0 ? 0.f : (float)G.end[h][quad - 1]) + rel);
                         } else {
 #pragma unroll
                             for (int e = 0; e < 16; ++e) pk[e] = 0u;
                         }
-                        ptx::tmem_st16(t_p + h * 64 + J * 16, pk);
+                        ptx::tmem_st16(t_p + J * 32 + h * 16, pk);
                     }
                 }
                 __syncwarp();
@@ -406,11 +389,11 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 if (!warp_wait(B_OQ, (uint32_t)i, 22)) break;
                 ptx::tc_fence_after();
                 // diag(2^L) Q S^T, onto which P V is added.
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
                     uint32_t ov[32];
                     ptx::tmem_ld32(t_o + c * 32, ov);
-                    const float gm = gamma[NH == 2 ? c >> 1 : 0];
+                    const float gm = NH == 2 && c >= 2 ? gamma[NH - 1] : gamma[0];
 #pragma unroll
                     for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(gm * __uint_as_float(ov[e]));
                     ptx::tmem_st32(t_o + c * 32, ov);
@@ -423,7 +406,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 ptx::tc_fence_after();
                 const int t = (c0 + i) * kC + r;
                 __nv_bfloat16 *row = a.o + ((size_t)(seq.x + t) * a.per_seq + item) * kC;
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
                     uint32_t ov[32];
                     ptx::tmem_ld32(t_o + c * 32, ov);
@@ -465,6 +448,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             st[4 * e + 3] = x.w;
         }
         if (!kState)
+#pragma unroll 1
             for (int s = 0; s < seg; ++s) {    // the segments before this one
                 const size_t p = (size_t)flat * (a.segments - 1) + s;
                 const float f = exp2f((float)a.seg_log[p * 2 + h]);
@@ -493,37 +477,52 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar(B_SOP));
         };
-        if (!kState && n > 0) copy_out();
         bool run = true;
         for (int i = 0; i < n; ++i) {
+            if (!kState || i > 0) copy_out();  // Q S^T of the last chunk was issued before its update and is done
             const Gates &G = gates[i & 1];
             const int x = load_v(i), valid = min(kC, len - (c0 + i) * kC);
             if (!(run = warp_wait(B_GF + (i & 1), (uint32_t)(i >> 1), 40) && warp_wait(B_F + x % kSlots, (uint32_t)(x / kSlots), 41))) break;
             const uint8_t *v = smem + (x % kSlots) * kTile + (r >> 6) * kHalf + (r & 7) * 2;
             const int chunk = (r & 63) >> 3;
-            for (int u = 0; u < 2 && run; ++u) {
+#pragma unroll 1
+            for (int u = 0; u < 2; ++u) {
                 const int s = 2 * u + wg, uses = 2 * i + u;
                 if (uses > 0 && !(run = warp_wait(B_WE + wg, (uint32_t)(uses - 1), 42))) break;
                 ptx::tc_fence_after();
-                uint32_t p0[16], p1[16], p2[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    float y[2];
-#pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        const int t = s * 32 + 2 * e + z;
-                        const uint16_t bits = *reinterpret_cast<const uint16_t *>(v + t * 128 + ((chunk ^ (t & 7)) << 4));
-                        y[z] = t < valid ? G.w[h][t] * __uint_as_float((uint32_t)bits << 16) : 0.f;
-                    }
-                    p0[e] = pack2(y[0], y[1]);
-                    const float a0 = y[0] - low(p0[e]), a1 = y[1] - high(p0[e]);
-                    p1[e] = pack2(a0, a1);
-                    p2[e] = pack2(a0 - low(p1[e]), a1 - high(p1[e]));
-                }
                 const uint32_t t_w = tmem + kColW + wg * 64 + lanes;
-                ptx::tmem_st16(t_w, p0);
-                ptx::tmem_st16(t_w + 16, p1);
-                ptx::tmem_st16(t_w + 32, p2);
+#pragma unroll 1
+                for (int z = 0; z < 2; ++z) {  // 16 tokens
+                    const int t0 = s * 32 + z * 16;
+                    float w[16], y[16];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float4 f = *reinterpret_cast<const float4 *>(&G.w[h][t0 + 4 * e]);
+                        w[4 * e] = f.x;
+                        w[4 * e + 1] = f.y;
+                        w[4 * e + 2] = f.z;
+                        w[4 * e + 3] = f.w;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const uint32_t bits = *reinterpret_cast<const uint16_t *>(v + (t0 + e) * 128 + ((chunk ^ (e & 7)) << 4));
+                        y[e] = w[e] * __uint_as_float(bits << 16);
+                    }
+                    if (t0 + 16 > valid)       // another sequence's rows
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) y[e] = t0 + e < valid ? y[e] : 0.f;
+                    uint32_t p0[8], p1[8], p2[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        p0[e] = pack2(y[2 * e], y[2 * e + 1]);
+                        const float a0 = y[2 * e] - low(p0[e]), a1 = y[2 * e + 1] - high(p0[e]);
+                        p1[e] = pack2(a0, a1);
+                        p2[e] = pack2(a0 - low(p1[e]), a1 - high(p1[e]));
+                    }
+                    ptx::tmem_st8(t_w + z * 8, p0);
+                    ptx::tmem_st8(t_w + 16 + z * 8, p1);
+                    ptx::tmem_st8(t_w + 32 + z * 8, p2);
+                }
                 ptx::tmem_wait_st();
                 ptx::tc_fence_before();
                 __syncwarp();
@@ -542,7 +541,6 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 #pragma unroll
                 for (int e = 0; e < 32; ++e) st[c * 32 + e] = fmaf(decay, st[c * 32 + e], __uint_as_float(d[e]));
             }
-            if (i + 1 < n) copy_out();         // Q S^T of this chunk was issued before its update and is done
         }
         float *dst = kState ? slots + (size_t)(seg + 1) * kC * kC
                             : last && a.S_new ? a.S_new + at : nullptr;
@@ -558,6 +556,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         ptx::mbar_wait(bar(B_DRAIN), 0);
     }
     if (warp == 0 && lane == 0 && aborted)
+#pragma unroll 1
         for (int x = max(0, loads - kSlots); x < loads; ++x) ptx::mbar_wait(bar(B_F + x % kSlots), (uint32_t)((x / kSlots) & 1));
     ptx::tc_fence_before();
     __syncthreads();

@@ -6,6 +6,7 @@
 #include <cuda_fp16.h>
 
 #include "stree_internal.cuh"
+#include "tc_ptx.cuh"
 
 namespace stree {
 
@@ -33,6 +34,38 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, int threads, size_t 
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, KArgs(args)...);
+}
+
+// The waits of a kernel's warp roles.  The first try is inlined; the bounded wait behind it
+// is one function of the kernel, since a copy at each of twenty waits made the roles' code
+// outgrow the instruction cache (the linear-attention prompt kernel ran ten times slower).
+struct Waits {
+    volatile int *aborted;                     // shared: a wait of the CTA has run out
+    int32_t *err;                              // error word, or NULL
+    int b;                                     // the sequence that it names
+};
+
+static __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int *aborted, int32_t *err, int b,
+                                              int where)
+{
+    if (*aborted) return false;
+    if (ptx::mbar_wait(bar, parity)) return true;
+    if (err) latch_error(err, STREE_ERR_TIMEOUT, b, where, (int)parity);
+    *aborted = 1;
+    return false;
+}
+
+// One thread waits for the phase with this parity (its lowest bit) to complete.
+__device__ __forceinline__ bool wait_one(const Waits &w, uint32_t bar, uint32_t parity, int where)
+{
+    return ptx::mbar_try_wait(bar, parity & 1) || wait_slow(bar, parity & 1, w.aborted, w.err, w.b, where);
+}
+
+// All lanes of a warp wait together, with one answer.
+__device__ __forceinline__ bool wait_warp(const Waits &w, uint32_t bar, uint32_t parity, int where)
+{
+    if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity & 1))) return true;
+    return __all_sync(0xffffffffu, wait_slow(bar, parity & 1, w.aborted, w.err, w.b, where));
 }
 
 // A sequence's packed rows [begin, end); an offset pair that is not ascending
