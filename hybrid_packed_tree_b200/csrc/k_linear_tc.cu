@@ -64,7 +64,8 @@ struct Gates {                                 // of one chunk, per head
     float beta[2][kC];
     float fac[2][kC];                          // 2^(L at the end of j's block - L_j) beta_j
     float w[2][kC];
-    double end[2][4];                          // L at the end of each 32-token block
+    double after[2][4];                        // log decay from the end of each 32-token block to the chunk's
+    double all[2];                             // of the whole chunk
 };
 
 struct TcArgs {
@@ -78,7 +79,8 @@ struct TcArgs {
     int total, batch, heads_v, heads_k, per_seq, segments;   // per_seq: 128-column items of a sequence
 };
 
-constexpr uint32_t kSmem = kSlots * kTile + kTile + 2 * sizeof(Gates) + 1024;
+constexpr uint32_t kStage = 4 * 32 * 128;       // rows of O on their way out, half a row at a time
+constexpr uint32_t kSmem = kSlots * kTile + kTile + kStage + 2 * sizeof(Gates) + 1024;
 
 // Rows [valid, 128) of a tile of tokens become zero (they belong to another sequence).
 __device__ __forceinline__ void zero_rows(uint8_t *tile, int valid, int lane)
@@ -97,6 +99,13 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
 __device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
@@ -114,10 +123,11 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     __shared__ uint32_t tmem_s;
     uint8_t *smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t *sop = smem + kSlots * kTile;      // the bf16 state, K-major
-    Gates *gates = reinterpret_cast<Gates *>(sop + kTile);
+    uint8_t *stage = sop + kTile;
+    Gates *gates = reinterpret_cast<Gates *>(stage + kStage);
     auto bar = [&](int i) { return ptx::smem_u32(&bars[i]); };
     const uint32_t ring = ptx::smem_u32(smem), sop_u = ptx::smem_u32(sop);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = ptx::warp_index();
 
     pdl_start();
     if (!kState && blockIdx.x == gridDim.x - 1) {   // the error word
@@ -185,6 +195,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             // ------------------------------------------------------------ MMA issue
             const uint32_t id_kk = ptx::idesc_bf16_kk(kC, kC), id_mn = ptx::idesc_bf16_bmn(kC, kC),
                            id_pv = ptx::idesc_bf16_bmn(kC, kDv);
+            const uint64_t d_s = ptx::desc_kmajor_sw128(sop_u);
             auto arrived = [&](int x, int where) { return warp_wait(B_F + x % kSlots, (uint32_t)(x / kSlots), where); };
             auto slot = [&](int x) { return ring + (x % kSlots) * kTile; };
             auto release = [&](int x) {        // a slot that another load will use
@@ -193,28 +204,31 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             bool ok = true;
             for (int i = 0; i < n && ok; ++i) {
                 const int valid = min(kC, len - (c0 + i) * kC);
-                const uint32_t k0 = slot(load_k(i)), q0 = slot(load_q(i)), v0 = slot(load_v(i));
+                // The descriptors of a tile's steps are made from one per tile.
+                const uint64_t d_q = ptx::desc_kmajor_sw128(slot(load_q(i))), d_k = ptx::desc_kmajor_sw128(slot(load_k(i))),
+                               d_kt = ptx::desc_mnmajor_sw128(slot(load_k(i)), kHalf, 1024),
+                               d_v = ptx::desc_mnmajor_sw128(slot(load_v(i)), kHalf, 1024);
                 if (!(ok = arrived(load_k(i), 10))) break;
                 if (valid < kC) zero_rows(smem + (load_k(i) % kSlots) * kTile, valid, lane);
                 if (!kState) {
                     if (!(ok = arrived(load_q(i), 11))) break;
-                    if (lane == 0) {
+                    if (ptx::elect_one()) {
                         ptx::tc_fence_after();
 #pragma unroll
                         for (int kk = 0; kk < kC / 16; ++kk)
-                            ptx::mma_f16(tmem + kColP, ptx::desc_kmajor_sw128(q0 + (kk >> 2) * kHalf + (kk & 3) * 32),
-                                         ptx::desc_kmajor_sw128(k0 + (kk >> 2) * kHalf + (kk & 3) * 32), id_kk, kk != 0);
+                            ptx::mma_f16(tmem + kColP, ptx::desc_at(d_q, (kk >> 2) * kHalf + (kk & 3) * 32),
+                                         ptx::desc_at(d_k, (kk >> 2) * kHalf + (kk & 3) * 32), id_kk, kk != 0);
                         ptx::mma_commit(bar(B_SF));
                     }
                     __syncwarp();
                     // Q S^T, once the state's copy is there and the last chunk's O has been read.
                     if (!(ok = warp_wait(B_SOP, (uint32_t)i, 12)) || (i > 0 && !(ok = warp_wait(B_OE, (uint32_t)(i - 1), 13)))) break;
-                    if (lane == 0) {
+                    if (ptx::elect_one()) {
                         ptx::tc_fence_after();
 #pragma unroll
                         for (int kk = 0; kk < kC / 16; ++kk)
-                            ptx::mma_f16(tmem + kColO, ptx::desc_kmajor_sw128(q0 + (kk >> 2) * kHalf + (kk & 3) * 32),
-                                         ptx::desc_kmajor_sw128(sop_u + (kk >> 2) * kHalf + (kk & 3) * 32), id_kk, kk != 0);
+                            ptx::mma_f16(tmem + kColO, ptx::desc_at(d_q, (kk >> 2) * kHalf + (kk & 3) * 32),
+                                         ptx::desc_at(d_s, (kk >> 2) * kHalf + (kk & 3) * 32), id_kk, kk != 0);
                         ptx::mma_commit(bar(B_OQ));
                         release(load_q(i));
                     }
@@ -226,42 +240,42 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 #pragma unroll 1
                 for (int s = 0; s < 4 && ok; ++s) {
                     if (!(ok = warp_wait(B_WF + (s & 1), (uint32_t)(2 * i + (s >> 1)), 14))) break;
-                    if (lane == 0) {
+                    if (ptx::elect_one()) {
                         ptx::tc_fence_after();
 #pragma unroll
                         for (int part = 0; part < 3; ++part)
 #pragma unroll
                             for (int kk = 0; kk < 2; ++kk)
                                 ptx::mma_f16_ta(tmem + kColD, tmem + kColW + (s & 1) * 64 + part * 16 + kk * 8,
-                                                ptx::desc_mnmajor_sw128(k0 + (2 * s + kk) * 2048, kHalf, 1024), id_mn,
+                                                ptx::desc_at(d_kt, (2 * s + kk) * 2048), id_mn,
                                                 (s | part | kk) != 0);
                         ptx::mma_commit(bar(B_WE + (s & 1)));
                     }
                     __syncwarp();
                 }
                 if (!ok) break;
-                if (lane == 0) {
+                if (ptx::elect_one()) {
                     ptx::mma_commit(bar(B_DF));
                     release(load_k(i));
                 }
                 __syncwarp();
                 if (kState) {
                     // The state warps have read V before they handed over its last part.
-                    if (lane == 0) release(load_v(i));
+                    if (ptx::elect_one()) release(load_v(i));
                     __syncwarp();
                     continue;
                 }
                 if (!(ok = arrived(load_v(i), 15))) break;
                 if (valid < kC) zero_rows(smem + (load_v(i) % kSlots) * kTile, valid, lane);
                 if (!(ok = warp_wait(B_PF, (uint32_t)i, 16))) break;
-                if (lane == 0) {
+                if (ptx::elect_one()) {
                     ptx::tc_fence_after();
 #pragma unroll
                     for (int hh = 0; hh < NH; ++hh)
 #pragma unroll
                         for (int kk = 0; kk < kC / 16; ++kk)
                             ptx::mma_f16_ta(tmem + kColO + hh * kDv, tmem + kColP + (kk >> 1) * 32 + hh * 16 + (kk & 1) * 8,
-                                            ptx::desc_mnmajor_sw128(v0 + hh * kHalf + kk * 2048, kHalf, 1024), id_pv, 1);
+                                            ptx::desc_at(d_v, hh * kHalf + kk * 2048), id_pv, 1);
                     ptx::mma_commit(bar(B_OF));
                     release(load_v(i));
                 }
@@ -270,59 +284,54 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         } else if (warp == 2) {
             // ------------------------------------------------------------ gates
             double total[2] = {0.0, 0.0};
-            float al[NH][4], be[NH][4];
-            auto fetch = [&](int i) {          // four tokens a lane
+            float al[NH][4], be[NH][4];        // of tokens lane + 32 J
+            auto fetch = [&](int i) {
 #pragma unroll
                 for (int h = 0; h < NH; ++h)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int t = (c0 + i) * kC + lane * 4 + e;
+                    for (int J = 0; J < 4; ++J) {
+                        const int t = (c0 + i) * kC + J * 32 + lane;
                         const size_t at = (size_t)(seq.x + t) * a.heads_v + head0 + h;
-                        al[h][e] = t < len ? __ldg(a.alpha + at) : 1.f;
-                        be[h][e] = t < len ? (a.beta ? __ldg(a.beta + at) : 1.f) : 0.f;   // weight zero past the end
+                        al[h][J] = t < len ? __ldg(a.alpha + at) : 1.f;
+                        be[h][J] = t < len ? (a.beta ? __ldg(a.beta + at) : 1.f) : 0.f;   // weight zero past the end
                     }
             };
             if (n > 0) fetch(0);
             for (int i = 0; i < n; ++i) {
                 if (i >= 2 && !warp_wait(B_GE + (i & 1), (uint32_t)((i >> 1) - 1), 30)) break;
                 Gates &G = gates[i & 1];
+                // A block of 32 tokens at a time, last to first: `after` is the log decay from its end
+                // to the chunk's end.
+                double after[2] = {0.0, 0.0};
+#pragma unroll 1
+                for (int x = 4 * NH - 1; x >= 0; --x) {
+                    const int h = NH == 2 ? x & 1 : 0, J = NH == 2 ? x >> 1 : x;
+                    float alpha = al[0][0], beta = be[0][0];
 #pragma unroll
-                for (int h = 0; h < NH; ++h) {
-                    double L[4], sum = 0.0;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float lg = log2f(al[h][e]);
-                        lg = lg < kLogZero ? kLogZero : lg;
-                        sum += (double)lg;
-                        L[e] = sum;
+                    for (int y = 1; y < 4 * NH; ++y) {
+                        alpha = x == y ? al[NH == 2 ? y & 1 : 0][NH == 2 ? y >> 1 : y] : alpha;
+                        beta = x == y ? be[NH == 2 ? y & 1 : 0][NH == 2 ? y >> 1 : y] : beta;
                     }
-                    double scan = sum;
+                    const float lg = log2f(alpha);
+                    double L = (double)(lg < kLogZero ? kLogZero : lg);
 #pragma unroll
                     for (int d = 1; d < 32; d <<= 1) {
-                        const double u = __shfl_up_sync(0xffffffffu, scan, d);
-                        if (lane >= d) scan += u;
+                        const double u = __shfl_up_sync(0xffffffffu, L, d);
+                        if (lane >= d) L += u;
                     }
-                    const double before = scan - sum;
-                    // Eight lanes are a block: its end, and the end of the block before it.
-                    const double blk_end = __shfl_sync(0xffffffffu, scan, lane | 7);
-                    const double prev = __shfl_sync(0xffffffffu, scan, max((lane & 24) - 1, 0));
-                    const double blk_start = lane < 8 ? 0.0 : prev, all = __shfl_sync(0xffffffffu, scan, 31);
-                    if ((lane & 7) == 7) G.end[h][lane >> 3] = scan;
-                    float4 rel, fac, w;
-                    float *rp = &rel.x, *fp = &fac.x, *wp = &w.x;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const double Le = before + L[e];
-                        rp[e] = (float)(Le - blk_start);
-                        fp[e] = exp2f((float)(blk_end - Le)) * be[h][e];
-                        wp[e] = exp2f((float)(all - Le)) * be[h][e];
-                    }
-                    *reinterpret_cast<float4 *>(&G.rel[h][lane * 4]) = rel;
-                    *reinterpret_cast<float4 *>(&G.fac[h][lane * 4]) = fac;
-                    *reinterpret_cast<float4 *>(&G.w[h][lane * 4]) = w;
-                    *reinterpret_cast<float4 *>(&G.beta[h][lane * 4]) = make_float4(be[h][0], be[h][1], be[h][2], be[h][3]);
-                    total[h] += all;
+                    const double end = __shfl_sync(0xffffffffu, L, 31), rest = h == 0 ? after[0] : after[1];
+                    const int j = J * 32 + lane;
+                    G.rel[h][j] = (float)L;
+                    G.beta[h][j] = beta;
+                    G.fac[h][j] = exp2f((float)(end - L)) * beta;
+                    G.w[h][j] = exp2f((float)(end - L + rest)) * beta;
+                    if (lane == 0) G.after[h][J] = rest;
+                    if (h == 0) after[0] += end;
+                    else after[1] += end;
                 }
+                if (lane < NH) G.all[lane] = lane == 0 ? after[0] : after[1];
+                total[0] += after[0];
+                total[1] += after[1];
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(bar(B_GF + (i & 1)));
                 if (i + 1 < n) fetch(i + 1);
@@ -347,18 +356,22 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 for (int J = 0; J < 4; ++J) {  // 32 tokens j: read the scores, write P over them
                     uint32_t sv[32];
                     if (J <= quad) ptx::tmem_ld32(t_p + J * 32, sv);
+                    const auto score = [&](int j) { return make_float2(__uint_as_float(sv[j]), __uint_as_float(sv[j + 1])); };
 #pragma unroll
                     for (int h = 0; h < NH; ++h) {
                         uint32_t pk[16];
                         const float rel = G.rel[h][r];
                         if (J < quad) {
-                            const float row = ptx::ex2_approx((float)(G.end[h][quad - 1] - G.end[h][J]) + rel);
+                            // L_i less L at the end of block J.
+                            const float row = ptx::ex2_approx((float)(G.after[h][J] - G.after[h][quad - 1]) + rel);
+                            const float2 row2 = make_float2(row, row);
 #pragma unroll
                             for (int e = 0; e < 8; ++e) {
                                 const float4 f = *reinterpret_cast<const float4 *>(&G.fac[h][J * 32 + 4 * e]);
-                                const uint32_t *x = &sv[4 * e];
-                                pk[2 * e] = pack2(__uint_as_float(x[0]) * (row * f.x), __uint_as_float(x[1]) * (row * f.y));
-                                pk[2 * e + 1] = pack2(__uint_as_float(x[2]) * (row * f.z), __uint_as_float(x[3]) * (row * f.w));
+                                const float2 x = ptx::fmul2(score(4 * e), ptx::fmul2(row2, make_float2(f.x, f.y)));
+                                const float2 y = ptx::fmul2(score(4 * e + 2), ptx::fmul2(row2, make_float2(f.z, f.w)));
+                                pk[2 * e] = pack2(x.x, x.y);
+                                pk[2 * e + 1] = pack2(y.x, y.y);
                             }
                         } else if (J == quad) {
 #pragma unroll
@@ -370,13 +383,12 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                                 for (int u = 0; u < 4; ++u) {
                                     const int j = 4 * e + u;
                                     const float f = ptx::ex2_approx(rel - (&rj.x)[u]) * (&bj.x)[u];
-                                    p[u] = j <= lane ? __uint_as_float(sv[j]) * f : 0.f;
-                                    if (j == lane) p[u] += skip[h];
+                                    p[u] = j <= lane ? fmaf(__uint_as_float(sv[j]), f, j == lane ? skip[h] : 0.f) : 0.f;
                                 }
                                 pk[2 * e] = pack2(p[0], p[1]);
                                 pk[2 * e + 1] = pack2(p[2], p[3]);
                             }
-                            gamma[h] = ptx::ex2_approx((quad == 0 ? 0.f : (float)G.end[h][quad - 1]) + rel);
+                            gamma[h] = ptx::ex2_approx((float)(quad == 0 ? 0.0 : G.all[h] - G.after[h][quad - 1]) + rel);
                         } else {
 #pragma unroll
                             for (int e = 0; e < 16; ++e) pk[e] = 0u;
@@ -395,7 +407,11 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     ptx::tmem_ld32(t_o + c * 32, ov);
                     const float gm = NH == 2 && c >= 2 ? gamma[NH - 1] : gamma[0];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(gm * __uint_as_float(ov[e]));
+                    for (int e = 0; e < 32; e += 2) {
+                        const float2 x = ptx::fmul2(make_float2(gm, gm), make_float2(__uint_as_float(ov[e]), __uint_as_float(ov[e + 1])));
+                        ov[e] = __float_as_uint(x.x);
+                        ov[e + 1] = __float_as_uint(x.y);
+                    }
                     ptx::tmem_st32(t_o + c * 32, ov);
                 }
                 ptx::tmem_wait_st();
@@ -404,24 +420,37 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 if (lane == 0) ptx::mbar_arrive(bar(B_PF));   // P written, Q S^T scaled
                 if (!warp_wait(B_OF, (uint32_t)i, 23)) break;
                 ptx::tc_fence_after();
-                const int t = (c0 + i) * kC + r;
-                __nv_bfloat16 *row = a.o + ((size_t)(seq.x + t) * a.per_seq + item) * kC;
-#pragma unroll 1
+                uint32_t out[64];              // the row in bf16: O's columns are free for the next chunk
+#pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     uint32_t ov[32];
                     ptx::tmem_ld32(t_o + c * 32, ov);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int u = 0; u < 4; ++u)
-                            w[u] = pack2(__uint_as_float(ov[8 * e + 2 * u]), __uint_as_float(ov[8 * e + 2 * u + 1]));
-                        if (t < len) *reinterpret_cast<uint4 *>(row + c * 32 + 8 * e) = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
+                    for (int e = 0; e < 16; ++e) out[c * 16 + e] = pack2(__uint_as_float(ov[2 * e]), __uint_as_float(ov[2 * e + 1]));
                 }
                 ptx::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(bar(B_OE));
+                // To global memory by way of shared memory, half a row at a time, so that a warp's
+                // store covers whole 128-byte lines (four rows) instead of 16 bytes of 32 rows.
+                uint8_t *mine = stage + quad * 4096;
+                __nv_bfloat16 *dst = a.o + ((size_t)(seq.x + (c0 + i) * kC + quad * 32) * a.per_seq + item) * kC;
+                const int rows = len - (c0 + i) * kC - quad * 32;
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        *reinterpret_cast<uint4 *>(mine + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+                            make_uint4(out[hh * 32 + 4 * c], out[hh * 32 + 4 * c + 1], out[hh * 32 + 4 * c + 2], out[hh * 32 + 4 * c + 3]);
+                    __syncwarp();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int row = e * 4 + (lane >> 3), c = lane & 7;
+                        const uint4 x = *reinterpret_cast<const uint4 *>(mine + row * 128 + ((c ^ (row & 7)) << 4));
+                        if (row < rows) *reinterpret_cast<uint4 *>(dst + (size_t)row * a.per_seq * kC + hh * 64 + c * 8) = x;
+                    }
+                    __syncwarp();
+                }
             }
         }
     } else {
@@ -483,8 +512,9 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             const Gates &G = gates[i & 1];
             const int x = load_v(i), valid = min(kC, len - (c0 + i) * kC);
             if (!(run = warp_wait(B_GF + (i & 1), (uint32_t)(i >> 1), 40) && warp_wait(B_F + x % kSlots, (uint32_t)(x / kSlots), 41))) break;
-            const uint8_t *v = smem + (x % kSlots) * kTile + (r >> 6) * kHalf + (r & 7) * 2;
-            const int chunk = (r & 63) >> 3;
+            // This lane's row address for ldmatrix: token lane % 8 of eight, the warp's columns 8 (lane / 8) ..
+            const uint32_t v = ring + (x % kSlots) * kTile + (quad >> 1) * kHalf + (lane & 7) * 128 +
+                               ((((quad & 1) * 4 + (lane >> 3)) ^ (lane & 7)) << 4);
 #pragma unroll 1
             for (int u = 0; u < 2; ++u) {
                 const int s = 2 * u + wg, uses = 2 * i + u;
@@ -493,35 +523,41 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 const uint32_t t_w = tmem + kColW + wg * 64 + lanes;
 #pragma unroll 1
                 for (int z = 0; z < 2; ++z) {  // 16 tokens
-                    const int t0 = s * 32 + z * 16;
-                    float w[16], y[16];
+                    // Transposed 8 x 8 tiles: a register is two tokens (2 (lane % 4), + 1) of column lane / 4.
+                    const int t0 = s * 32 + z * 16, t = t0 + (lane & 3) * 2;
+                    uint32_t raw[2][4];
+                    ldsm4_t(v + t0 * 128, raw[0]);
+                    ldsm4_t(v + t0 * 128 + 1024, raw[1]);
+                    const float2 w[2] = {*reinterpret_cast<const float2 *>(&G.w[h][t]), *reinterpret_cast<const float2 *>(&G.w[h][t + 8])};
+                    float2 y[2][4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float4 f = *reinterpret_cast<const float4 *>(&G.w[h][t0 + 4 * e]);
-                        w[4 * e] = f.x;
-                        w[4 * e + 1] = f.y;
-                        w[4 * e + 2] = f.z;
-                        w[4 * e + 3] = f.w;
-                    }
+                    for (int e = 0; e < 2; ++e)
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const uint32_t bits = *reinterpret_cast<const uint16_t *>(v + (t0 + e) * 128 + ((chunk ^ (e & 7)) << 4));
-                        y[e] = w[e] * __uint_as_float(bits << 16);
-                    }
+                        for (int c = 0; c < 4; ++c) y[e][c] = ptx::fmul2(w[e], make_float2(low(raw[e][c]), high(raw[e][c])));
                     if (t0 + 16 > valid)       // another sequence's rows
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) y[e] = t0 + e < valid ? y[e] : 0.f;
-                    uint32_t p0[8], p1[8], p2[8];
+                        for (int e = 0; e < 2; ++e)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        p0[e] = pack2(y[2 * e], y[2 * e + 1]);
-                        const float a0 = y[2 * e] - low(p0[e]), a1 = y[2 * e + 1] - high(p0[e]);
-                        p1[e] = pack2(a0, a1);
-                        p2[e] = pack2(a0 - low(p1[e]), a1 - high(p1[e]));
+                            for (int c = 0; c < 4; ++c) {
+                                y[e][c].x = t + 8 * e < valid ? y[e][c].x : 0.f;
+                                y[e][c].y = t + 8 * e + 1 < valid ? y[e][c].y : 0.f;
+                            }
+                    // Three parts of eight bits each, cut off rather than rounded: their sum is exact.
+#pragma unroll
+                    for (int part = 0; part < 3; ++part) {
+                        uint32_t p[2][4];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                const uint32_t bx = __float_as_uint(y[e][c].x), by = __float_as_uint(y[e][c].y);
+                                p[e][c] = __byte_perm(bx, by, 0x7632);
+                                if (part < 2)
+                                    y[e][c] = ptx::ffma2(make_float2(low(p[e][c]), high(p[e][c])), make_float2(-1.f, -1.f), y[e][c]);
+                            }
+                        ptx::tmem_st16x8(t_w + part * 16 + z * 8, p[0][0], p[0][1], p[1][0], p[1][1]);
+                        ptx::tmem_st16x8(t_w + (16u << 16) + part * 16 + z * 8, p[0][2], p[0][3], p[1][2], p[1][3]);
                     }
-                    ptx::tmem_st8(t_w + z * 8, p0);
-                    ptx::tmem_st8(t_w + 16 + z * 8, p1);
-                    ptx::tmem_st8(t_w + 32 + z * 8, p2);
                 }
                 ptx::tmem_wait_st();
                 ptx::tc_fence_before();
@@ -529,7 +565,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 if (lane == 0) ptx::mbar_arrive(bar(B_WF + wg));
             }
             if (!run) break;
-            const float decay = exp2f((float)G.end[h][3]);
+            const float decay = exp2f((float)G.all[h]);
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar(B_GE + (i & 1)));
             if (!(run = warp_wait(B_DF, (uint32_t)i, 43))) break;
@@ -539,7 +575,12 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 uint32_t d[32];
                 ptx::tmem_ld32(tmem + kColD + wg * 64 + c * 32 + lanes, d);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) st[c * 32 + e] = fmaf(decay, st[c * 32 + e], __uint_as_float(d[e]));
+                for (int e = 0; e < 32; e += 2) {
+                    const float2 x = ptx::ffma2(make_float2(decay, decay), make_float2(st[c * 32 + e], st[c * 32 + e + 1]),
+                                                make_float2(__uint_as_float(d[e]), __uint_as_float(d[e + 1])));
+                    st[c * 32 + e] = x.x;
+                    st[c * 32 + e + 1] = x.y;
+                }
             }
         }
         float *dst = kState ? slots + (size_t)(seg + 1) * kC * kC
@@ -551,7 +592,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     }
 
     // -------------------------------------------------------------------- teardown
-    if (warp == 1 && lane == 0 && aborted) {
+    if (warp == 1 && aborted && ptx::elect_one()) {
         ptx::mma_commit(bar(B_DRAIN));         // every issued MMA completes first
         ptx::mbar_wait(bar(B_DRAIN), 0);
     }
