@@ -148,9 +148,8 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const bool last = seg == a.segments - 1;
     if (n == 0 && !kState && !last) return;    // nothing to put out
 
-    const Waits waits{&aborted, a.err, b};
-    auto wait = [&](int i, uint32_t parity, int where) { return wait_one(waits, bar(i), parity, where); };
-    auto warp_wait = [&](int i, uint32_t parity, int where) { return wait_warp(waits, bar(i), parity, where); };
+    auto wait = [&](int i, uint32_t parity, int where) { return wait_one(&aborted, bar(i), parity, where); };
+    auto warp_wait = [&](int i, uint32_t parity, int where) { return wait_warp(&aborted, bar(i), parity, where); };
     if (tid == 0) {
         ptx::prefetch_tensormap(&tm_q);
         ptx::prefetch_tensormap(&tm_k);
@@ -180,16 +179,19 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 
     int loads = 0;
     if (warp < 4) {
-        if (warp == 0 && lane == 0) {
-            // ------------------------------------------------------------ producer
-            for (; loads < kLoads * n; ++loads) {
-                const int s = loads % kSlots, i = loads / kLoads, what = loads % kLoads;
-                if (loads >= kSlots && !wait(B_E + s, (uint32_t)(loads / kSlots - 1), 1)) break;
-                const bool is_v = what == kLoads - 1;
-                const CUtensorMap *m = is_v ? &tm_v : what == 0 ? &tm_k : &tm_q;
-                ptx::mbar_expect_tx(bar(B_F + s), kTile);
-                for (int hh = 0; hh < 2; ++hh)
-                    ptx::tma_load_3d(ring + s * kTile + hh * kHalf, m, hh * 64, is_v ? item : g, seq.x + (c0 + i) * kC, bar(B_F + s));
+        if (warp == 0) {
+            if (ptx::elect_one()) {
+                // ------------------------------------------------------------ producer
+#pragma unroll 1
+                for (; loads < kLoads * n; ++loads) {
+                    const int s = loads % kSlots, i = loads / kLoads, what = loads % kLoads;
+                    if (loads >= kSlots && !wait(B_E + s, (uint32_t)(loads / kSlots - 1), 1)) break;
+                    const bool is_v = what == kLoads - 1;
+                    const CUtensorMap *m = is_v ? &tm_v : what == 0 ? &tm_k : &tm_q;
+                    ptx::mbar_expect_tx(bar(B_F + s), kTile);
+                    for (int hh = 0; hh < 2; ++hh)
+                        ptx::tma_load_3d(ring + s * kTile + hh * kHalf, m, hh * 64, is_v ? item : g, seq.x + (c0 + i) * kC, bar(B_F + s));
+                }
             }
         } else if (warp == 1) {
             // ------------------------------------------------------------ MMA issue
@@ -202,6 +204,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 if (x + kSlots < kLoads * n) ptx::mma_commit(bar(B_E + x % kSlots));
             };
             bool ok = true;
+#pragma unroll 1
             for (int i = 0; i < n && ok; ++i) {
                 const int valid = min(kC, len - (c0 + i) * kC);
                 // The descriptors of a tile's steps are made from one per tile.
@@ -297,6 +300,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     }
             };
             if (n > 0) fetch(0);
+#pragma unroll 1
             for (int i = 0; i < n; ++i) {
                 if (i >= 2 && !warp_wait(B_GE + (i & 1), (uint32_t)((i >> 1) - 1), 30)) break;
                 Gates &G = gates[i & 1];
@@ -347,6 +351,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             float skip[NH];
 #pragma unroll
             for (int h = 0; h < NH; ++h) skip[h] = a.skip ? __ldg(a.skip + head0 + h) : 0.f;
+#pragma unroll 1
             for (int i = 0; i < n; ++i) {
                 const Gates &G = gates[i & 1];
                 if (!warp_wait(B_GF + (i & 1), (uint32_t)(i >> 1), 20) || !warp_wait(B_SF, (uint32_t)i, 21)) break;
@@ -507,6 +512,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             if (lane == 0) ptx::mbar_arrive(bar(B_SOP));
         };
         bool run = true;
+#pragma unroll 1
         for (int i = 0; i < n; ++i) {
             if (!kState || i > 0) copy_out();  // Q S^T of the last chunk was issued before its update and is done
             const Gates &G = gates[i & 1];
@@ -592,11 +598,12 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     }
 
     // -------------------------------------------------------------------- teardown
+    if (tid == 64 && aborted && a.err) latch_error(a.err, STREE_ERR_TIMEOUT, b, aborted, 0);
     if (warp == 1 && aborted && ptx::elect_one()) {
         ptx::mma_commit(bar(B_DRAIN));         // every issued MMA completes first
         ptx::mbar_wait(bar(B_DRAIN), 0);
     }
-    if (warp == 0 && lane == 0 && aborted)
+    if (warp == 0 && aborted && loads > 0)
 #pragma unroll 1
         for (int x = max(0, loads - kSlots); x < loads; ++x) ptx::mbar_wait(bar(B_F + x % kSlots), (uint32_t)((x / kSlots) & 1));
     ptx::tc_fence_before();

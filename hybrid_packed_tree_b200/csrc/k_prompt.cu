@@ -66,7 +66,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     uint8_t *smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
     auto bar = [&](int i) { return ptx::smem_u32(&bars[i]); };
     const uint32_t q0 = ptx::smem_u32(smem), ring = q0 + 2 * kTile;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = ptx::warp_index();
 
     pdl_start();
     if (blockIdx.x == gridDim.x - 1) {         // the error word
@@ -98,13 +98,8 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     }
     const int n = max(n_half[0], n_half[1]);
 
-    auto wait = [&](int i, uint32_t parity, int where) -> bool {
-        if (aborted) return false;
-        if (ptx::mbar_wait(bar(i), parity)) return true;
-        if (a.err) latch_error(a.err, STREE_ERR_TIMEOUT, b, where, (int)parity);
-        aborted = 1;
-        return false;
-    };
+    auto wait = [&](int i, uint32_t parity, int where) { return wait_one(&aborted, bar(i), parity, where); };
+    auto warp_wait = [&](int i, uint32_t parity, int where) { return wait_warp(&aborted, bar(i), parity, where); };
     if (tid == 0) {
         ptx::prefetch_tensormap(&tm_q);
         ptx::prefetch_tensormap(&tm_k);
@@ -125,82 +120,81 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     int loads = 0;
     if (warp < 4) {
         ptx::regs_less<56>();
-        if (warp == 0 && lane == 0) {
-            // ------------------------------------------------------------ producer
-            const uint32_t q_bytes = (uint32_t)(a.group * a.tokens) * 256u;
-            ptx::mbar_expect_tx(bar(B_QF), q_bytes * (n_half[1] ? 2 : 1));
-            for (int i = 0; i < (n_half[1] ? 2 : 1); ++i)
-                for (int hh = 0; hh < 2; ++hh)
-                    ptx::tma_load_3d(q0 + i * kTile + hh * kHalf, &tm_q, hh * 64, g * a.group, seq.x + t0 + i * a.tokens, bar(B_QF));
-            for (; loads < 2 * n; ++loads) {
-                const int s = loads % kSlots;
-                if (loads >= kSlots && !wait(B_E + s, (uint32_t)((loads / kSlots - 1) & 1), 1)) break;
-                ptx::mbar_expect_tx(bar(B_F + s), kTile);
-                const CUtensorMap *m = loads & 1 ? &tm_v : &tm_k;
-                for (int hh = 0; hh < 2; ++hh)
-                    ptx::tma_load_3d(ring + s * kTile + hh * kHalf, m, hh * 64, g, seq.x + (loads >> 1) * kKB, bar(B_F + s));
+        if (warp == 0) {
+            if (ptx::elect_one()) {
+                // -------------------------------------------------------- producer
+                const uint32_t q_bytes = (uint32_t)(a.group * a.tokens) * 256u;
+                const int halves = n_half[1] ? 2 : 1;
+                ptx::mbar_expect_tx(bar(B_QF), q_bytes * halves);
+                for (int i = 0; i < halves; ++i)
+                    for (int hh = 0; hh < 2; ++hh)
+                        ptx::tma_load_3d(q0 + i * kTile + hh * kHalf, &tm_q, hh * 64, g * a.group, seq.x + t0 + i * a.tokens, bar(B_QF));
+#pragma unroll 1
+                for (; loads < 2 * n; ++loads) {
+                    const int s = loads % kSlots;
+                    if (loads >= kSlots && !wait(B_E + s, (uint32_t)(loads / kSlots - 1), 1)) break;
+                    ptx::mbar_expect_tx(bar(B_F + s), kTile);
+                    const CUtensorMap *m = loads & 1 ? &tm_v : &tm_k;
+                    for (int hh = 0; hh < 2; ++hh)
+                        ptx::tma_load_3d(ring + s * kTile + hh * kHalf, m, hh * 64, g, seq.x + (loads >> 1) * kKB, bar(B_F + s));
+                }
             }
         } else if (warp == 1) {
             // ------------------------------------------------------------ MMA issue
             const uint32_t id_s = ptx::idesc_bf16_kk(kM, kKB), id_o = ptx::idesc_bf16_bmn(kM, kD);
-            bool ok = true;
-            auto all = [&](bool x) { return __shfl_sync(0xffffffffu, x ? 1 : 0, 0) != 0; };
             // Load number x (K of block i: 2 i, V: 2 i + 1) has arrived.
-            auto arrived = [&](int x) -> bool {
-                bool r = true;
-                if (lane == 0) r = wait(B_F + x % kSlots, (uint32_t)((x / kSlots) & 1), 10);
-                return all(r);
-            };
+            auto arrived = [&](int x) { return warp_wait(B_F + x % kSlots, (uint32_t)(x / kSlots), 10); };
             auto scores = [&](int half, int i) {
-                const uint32_t k0 = ring + (2 * i % kSlots) * kTile, qh = q0 + half * kTile;
+                const uint64_t d_q = ptx::desc_kmajor_sw128(q0 + half * kTile),
+                               d_k = ptx::desc_kmajor_sw128(ring + (2 * i % kSlots) * kTile);
 #pragma unroll
                 for (int kk = 0; kk < kD / 16; ++kk)
-                    ptx::mma_f16(tmem + half * kKB, ptx::desc_kmajor_sw128(qh + (kk >> 2) * kHalf + (kk & 3) * 32),
-                                 ptx::desc_kmajor_sw128(k0 + (kk >> 2) * kHalf + (kk & 3) * 32), id_s, kk != 0);
+                    ptx::mma_f16(tmem + half * kKB, ptx::desc_at(d_q, (kk >> 2) * kHalf + (kk & 3) * 32),
+                                 ptx::desc_at(d_k, (kk >> 2) * kHalf + (kk & 3) * 32), id_s, kk != 0);
                 ptx::mma_commit(bar(B_SF + half));
             };
             auto values = [&](int half, int i) {
-                const uint32_t v0 = ring + ((2 * i + 1) % kSlots) * kTile;
+                const uint64_t d_v = ptx::desc_mnmajor_sw128(ring + ((2 * i + 1) % kSlots) * kTile, kHalf, 1024);
 #pragma unroll
                 for (int kk = 0; kk < kKB / 16; ++kk)
-                    ptx::mma_f16_ta(tmem + 256 + half * kD, tmem + half * kKB + kk * 8,
-                                    ptx::desc_mnmajor_sw128(v0 + kk * 2048, kHalf, 1024), id_o, (i | kk) != 0);
+                    ptx::mma_f16_ta(tmem + 256 + half * kD, tmem + half * kKB + kk * 8, ptx::desc_at(d_v, kk * 2048), id_o,
+                                    (i | kk) != 0);
                 if (i == n_half[half] - 1) ptx::mma_commit(bar(B_OF + half));
             };
-            if (lane == 0) ok = wait(B_QF, 0, 11);
-            ok = all(ok) && arrived(0);
-            if (ok && lane == 0) {
+            bool ok = warp_wait(B_QF, 0, 11) && arrived(0);
+            if (ok && ptx::elect_one()) {
                 ptx::tc_fence_after();
+#pragma unroll
                 for (int half = 0; half < 2; ++half)
                     if (n_half[half]) scores(half, 0);
                 if (kSlots < 2 * n) ptx::mma_commit(bar(B_E + 0));
             }
+#pragma unroll 1
             for (int i = 0; i < n && ok; ++i) {
                 if (!(ok = arrived(2 * i + 1))) break;
                 const int valid = len - i * kKB;
                 if (valid < kKB) {             // the rows behind the sequence's end
                     uint8_t *v = smem + 2 * kTile + ((2 * i + 1) % kSlots) * kTile;
+#pragma unroll 1
                     for (int e = lane; e < (kKB - valid) * 16; e += 32) {
                         const int r = valid + e / 16, c = e % 16;
                         *reinterpret_cast<uint4 *>(v + (c >> 3) * kHalf + r * 128 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
                     }
                     ptx::fence_proxy_async_smem();
-                    __syncwarp();
                 }
                 if (i + 1 < n && !(ok = arrived(2 * i + 2))) break;
-                for (int half = 0; half < 2 && ok; ++half) {
-                    if (i >= n_half[half]) continue;
-                    if (lane == 0) {
-                        ok = wait(B_PF + half, (uint32_t)(i & 1), 12);
-                        if (ok) {
-                            ptx::tc_fence_after();
-                            values(half, i);
-                            if (i + 1 < n_half[half]) scores(half, i + 1);
-                        }
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    if (i >= n_half[half] || !ok) continue;
+                    if (!(ok = warp_wait(B_PF + half, (uint32_t)i, 12))) continue;
+                    if (ptx::elect_one()) {
+                        ptx::tc_fence_after();
+                        values(half, i);
+                        if (i + 1 < n_half[half]) scores(half, i + 1);
                     }
-                    ok = all(ok);
+                    __syncwarp();
                 }
-                if (ok && lane == 0) {         // slots that another load will use
+                if (ok && ptx::elect_one()) {  // slots that another load will use
                     if (2 * i + 1 + kSlots < 2 * n) ptx::mma_commit(bar(B_E + (2 * i + 1) % kSlots));
                     if (2 * i + 2 + kSlots < 2 * n) ptx::mma_commit(bar(B_E + (2 * i + 2) % kSlots));
                 }
@@ -210,7 +204,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     } else {
         // ---------------------------------------------------------------- softmax
         ptx::regs_more<224>();
-        const int half = (warp >> 2) - 1, quad = warp & 3, nh = n_half[half];
+        const int half = (warp >> 2) - 1, quad = warp & 3, nh = half ? n_half[1] : n_half[0];
         const int r = quad * 32 + lane;        // query row = tensor-memory lane
         const int token = t0 + half * a.tokens + r / a.group;
         const bool real = r < a.group * a.tokens && token < len;
@@ -221,9 +215,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         float m = -INFINITY, l = 0.f;
         bool run = true;
         for (int i = 0; i < nh; ++i) {
-            if (lane == 0) run = wait(B_SF + half, (uint32_t)(i & 1), 20);
-            run = __shfl_sync(0xffffffffu, run ? 1 : 0, 0) != 0;
-            if (!run) break;
+            if (!(run = warp_wait(B_SF + half, (uint32_t)i, 20))) break;
             ptx::tc_fence_after();
             uint32_t sv[kKB];
             ptx::tmem_ld128(t_s, sv);
@@ -281,11 +273,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar(B_PF + half));
         }
-        if (nh && run) {
-            if (lane == 0) run = wait(B_OF + half, 0, 21);
-            run = __shfl_sync(0xffffffffu, run ? 1 : 0, 0) != 0;
-        }
-        if (nh && run) {
+        if (nh && run && warp_wait(B_OF + half, 0, 21)) {
             ptx::tc_fence_after();
             uint32_t ov[kD];
             ptx::tmem_ld128(t_o, ov);
@@ -308,12 +296,14 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     }
 
     // -------------------------------------------------------------------- teardown
-    if (warp == 1 && lane == 0 && aborted) {
+    if (tid == 64 && aborted && a.err) latch_error(a.err, STREE_ERR_TIMEOUT, b, aborted, 0);
+    if (warp == 1 && aborted && ptx::elect_one()) {
         ptx::mma_commit(bar(B_DRAIN));         // every issued MMA completes first
         ptx::mbar_wait(bar(B_DRAIN), 0);
     }
-    if (warp == 0 && lane == 0 && aborted) {
+    if (warp == 0 && aborted) {
         ptx::mbar_wait(bar(B_QF), 0);
+#pragma unroll 1
         for (int x = max(0, loads - kSlots); x < loads; ++x) ptx::mbar_wait(bar(B_F + x % kSlots), (uint32_t)((x / kSlots) & 1));
     }
     ptx::tc_fence_before();

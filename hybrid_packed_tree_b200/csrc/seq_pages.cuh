@@ -36,36 +36,29 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, int threads, size_t 
     return cudaLaunchKernelEx(&cfg, kernel, KArgs(args)...);
 }
 
-// The waits of a kernel's warp roles.  The first try is inlined; the bounded wait behind it
-// is one function of the kernel, since a copy at each of twenty waits made the roles' code
-// outgrow the instruction cache (the linear-attention prompt kernel ran ten times slower).
-struct Waits {
-    volatile int *aborted;                     // shared: a wait of the CTA has run out
-    int32_t *err;                              // error word, or NULL
-    int b;                                     // the sequence that it names
-};
-
-static __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int *aborted, int32_t *err, int b,
-                                              int where)
+// The waits of a kernel's warp roles: bounded (about a second), and small, since a copy of the
+// code stands at each of some twenty waits and several roles share the instruction cache.  A
+// wait that runs out leaves its number in `aborted` (a shared int, zero before); every other
+// wait of the CTA then gives up too, and the kernel's end reports it.
+__device__ __forceinline__ bool wait_one(volatile int *aborted, uint32_t bar, uint32_t parity, int where)
 {
-    if (*aborted) return false;
-    if (ptx::mbar_wait(bar, parity)) return true;
-    if (err) latch_error(err, STREE_ERR_TIMEOUT, b, where, (int)parity);
-    *aborted = 1;
-    return false;
-}
-
-// One thread waits for the phase with this parity (its lowest bit) to complete.
-__device__ __forceinline__ bool wait_one(const Waits &w, uint32_t bar, uint32_t parity, int where)
-{
-    return ptx::mbar_try_wait(bar, parity & 1) || wait_slow(bar, parity & 1, w.aborted, w.err, w.b, where);
+    if (ptx::mbar_try_wait(bar, parity & 1)) return true;
+    const uint32_t t0 = ptx::globaltimer_lo();
+#pragma unroll 1
+    while (!ptx::mbar_try_wait(bar, parity & 1)) {
+        if (*aborted) return false;
+        if (ptx::globaltimer_lo() - t0 > (uint32_t)ptx::kWaitLimitNs) {
+            *aborted = where;
+            return false;
+        }
+    }
+    return true;
 }
 
 // All lanes of a warp wait together, with one answer.
-__device__ __forceinline__ bool wait_warp(const Waits &w, uint32_t bar, uint32_t parity, int where)
+__device__ __forceinline__ bool wait_warp(volatile int *aborted, uint32_t bar, uint32_t parity, int where)
 {
-    if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity & 1))) return true;
-    return __all_sync(0xffffffffu, wait_slow(bar, parity & 1, w.aborted, w.err, w.b, where));
+    return __all_sync(0xffffffffu, wait_one(aborted, bar, parity, where));
 }
 
 // A sequence's packed rows [begin, end); an offset pair that is not ascending
