@@ -18,7 +18,10 @@
 //     O += P V with P read from tensor memory (it lies over S: no shared memory is spent
 //     on it, and S of the next block follows P V of this one in the pipe's order);
 //   * two softmax warpgroups, one per half, one query row per thread: the row's 128
-//     scores by one load, mask, maximum, exponentials, P in bf16 back to tensor memory.
+//     scores by one load, mask, maximum, exponentials, P in bf16 back to tensor memory,
+//     32 keys at a time, so that P V of the first keys runs beside the exponentials of the
+//     last (8192 tokens of 32 heads over 8: 467 us handed over whole, 426 in two parts, 422 in
+//     four, 522 in eight; exponentials partly by a cubic on the FMA pipe gained nothing more).
 // The reference maximum moves only when a block exceeds it by 2^8 (output and sum are then
 // rescaled together): P stays below 256 and O / l is the same softmax.  Scores and sums are
 // fp32; P is rounded to bf16, the type of the values it multiplies.
@@ -42,9 +45,10 @@ constexpr int kSlots = 5;
 constexpr uint32_t kTile = 128 * 128 * 2, kHalf = kTile / 2;
 constexpr float kLazyLog2 = 8.f;
 constexpr uint32_t kSmem = 2 * kTile + kSlots * kTile + 1024;
+constexpr int kParts = 4;                      // parts in which a block's P is handed over
 constexpr int kMaxDevices = 64;
 
-enum Bars { B_QF = 0, B_F = 1, B_E = B_F + kSlots, B_SF = B_E + kSlots, B_PF = B_SF + 2, B_OF = B_PF + 2, B_DRAIN = B_OF + 2, kBars };
+enum Bars { B_QF = 0, B_F = 1, B_E = B_F + kSlots, B_SF = B_E + kSlots, B_PF = B_SF + 2, B_OF = B_PF + 2 * kParts, B_DRAIN = B_OF + 2, kBars };
 
 struct PromptArgs {
     const int32_t *cu;
@@ -104,7 +108,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         ptx::prefetch_tensormap(&tm_q);
         ptx::prefetch_tensormap(&tm_k);
         ptx::prefetch_tensormap(&tm_v);
-        for (int i = 0; i < kBars; ++i) ptx::mbar_init(bar(i), i == B_PF || i == B_PF + 1 ? 4 : 1);
+        for (int i = 0; i < kBars; ++i) ptx::mbar_init(bar(i), i >= B_PF && i < B_OF ? 4 : 1);
         ptx::fence_mbar_init();
         aborted = 0;
     }
@@ -153,13 +157,14 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                                  ptx::desc_at(d_k, (kk >> 2) * kHalf + (kk & 3) * 32), id_s, kk != 0);
                 ptx::mma_commit(bar(B_SF + half));
             };
-            auto values = [&](int half, int i) {
+            // A part of a block's keys: P is handed over in parts.
+            auto values = [&](int half, int i, int part) {
                 const uint64_t d_v = ptx::desc_mnmajor_sw128(ring + ((2 * i + 1) % kSlots) * kTile, kHalf, 1024);
 #pragma unroll
-                for (int kk = 0; kk < kKB / 16; ++kk)
+                for (int kk = part * (8 / kParts); kk < (part + 1) * (8 / kParts); ++kk)
                     ptx::mma_f16_ta(tmem + 256 + half * kD, tmem + half * kKB + kk * 8, ptx::desc_at(d_v, kk * 2048), id_o,
                                     (i | kk) != 0);
-                if (i == n_half[half] - 1) ptx::mma_commit(bar(B_OF + half));
+                if (part == kParts - 1 && i == n_half[half] - 1) ptx::mma_commit(bar(B_OF + half));
             };
             bool ok = warp_wait(B_QF, 0, 11) && arrived(0);
             if (ok && ptx::elect_one()) {
@@ -186,13 +191,16 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     if (i >= n_half[half] || !ok) continue;
-                    if (!(ok = warp_wait(B_PF + half, (uint32_t)i, 12))) continue;
-                    if (ptx::elect_one()) {
-                        ptx::tc_fence_after();
-                        values(half, i);
-                        if (i + 1 < n_half[half]) scores(half, i + 1);
+#pragma unroll
+                    for (int part = 0; part < kParts; ++part) {
+                        if (!ok || !(ok = warp_wait(B_PF + kParts * half + part, (uint32_t)i, 12))) continue;
+                        if (ptx::elect_one()) {
+                            ptx::tc_fence_after();
+                            values(half, i, part);
+                            if (part == kParts - 1 && i + 1 < n_half[half]) scores(half, i + 1);
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
                 }
                 if (ok && ptx::elect_one()) {  // slots that another load will use
                     if (2 * i + 1 + kSlots < 2 * n) ptx::mma_commit(bar(B_E + (2 * i + 1) % kSlots));
@@ -252,26 +260,27 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             }
             const float ref = m == -INFINITY ? 0.f : m;
             const float2 scale2 = make_float2(a.scale_log2, a.scale_log2), ref2 = make_float2(-ref, -ref);
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t pk[32];
+            for (int c = 0; c < kParts; ++c) {
+                constexpr int kPairs = kKB / 2 / kParts;
+                uint32_t pk[kPairs];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    const int key = c * 64 + 2 * e;
+                for (int e = 0; e < kPairs; ++e) {
+                    const int key = 2 * (c * kPairs + e);
                     const float2 x = ptx::ffma2(make_float2(__uint_as_float(sv[key]), __uint_as_float(sv[key + 1])), scale2, ref2);
-                    const float p0 = ptx::ex2_approx(x.x), p1 = ptx::ex2_approx(x.y);
-                    sum[e & 3] += p0 + p1;
-                    const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
+                    const float2 q = make_float2(ptx::ex2_approx(x.x), ptx::ex2_approx(x.y));
+                    sum[e & 1] = ptx::fadd2(sum[e & 1], q);
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(q.x, q.y);
                     pk[e] = *reinterpret_cast<const uint32_t *>(&h);
                 }
-                ptx::tmem_st32(t_s + c * 32, pk);
+                ptx::tmem_st16(t_s + c * kPairs, pk);
+                ptx::tmem_wait_st();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar(B_PF + kParts * half + c));
             }
-            l = l * f + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
-            ptx::tmem_wait_st();
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(bar(B_PF + half));
+            l = l * f + ((sum[0].x + sum[1].x) + (sum[0].y + sum[1].y));
         }
         if (nh && run && warp_wait(B_OF + half, 0, 21)) {
             ptx::tc_fence_after();
