@@ -120,6 +120,14 @@ __global__ void __launch_bounds__(kThreads) linear_prompt_kernel(const LinearArg
     __shared__ float qs[kTile][CH * 128], ks[kTile][CH * 128], vs[kTile][kWarps * kRows];
     __shared__ float al[kTile], be[kTile];
     pdl_start();
+    if (blockIdx.x == gridDim.x - 1) {         // the error word
+        PageCheck c{};
+        c.cu = a.cu;
+        c.batch = a.batch;
+        c.total = a.total;
+        check_pages(c, a.err);
+        return;
+    }
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int slices = (a.dv + kWarps * kRows - 1) / (kWarps * kRows);
     const int sl = blockIdx.x % slices;
@@ -200,16 +208,6 @@ __global__ void __launch_bounds__(kThreads) linear_prompt_kernel(const LinearArg
         }
 }
 
-__global__ void __launch_bounds__(kThreads) linear_check_kernel(const LinearArgs a)
-{
-    pdl_start();
-    PageCheck c{};
-    c.cu = a.cu;
-    c.batch = a.batch;
-    c.total = a.total;
-    check_pages(c, a.err);
-}
-
 template <typename T>
 cudaError_t launch_step(const LinearArgs &a, cudaStream_t s)
 {
@@ -223,7 +221,7 @@ template <typename T>
 cudaError_t launch_prompt(const LinearArgs &a, cudaStream_t s)
 {
     const int slices = (a.dv + kWarps * kRows - 1) / (kWarps * kRows);
-    const dim3 grid((unsigned)((long long)a.batch * a.heads_v * slices));
+    const dim3 grid((unsigned)((long long)a.batch * a.heads_v * slices + 1));
     return a.dk <= 128 ? launch_pdl(linear_prompt_kernel<T, 1>, grid, kThreads, 0, s, a)
                        : launch_pdl(linear_prompt_kernel<T, 2>, grid, kThreads, 0, s, a);
 }
@@ -324,7 +322,6 @@ extern "C" stree_status stree_linear_prompt(const void *q, const void *k, const 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (linear_tc_supported(heads_v, heads_k, dk, dv, dtype))
         return launch_linear_tc(a, workspace, workspace_bytes, s) == cudaSuccess ? STREE_OK : STREE_ERR_CUDA;
-    if (err_out && launch_pdl(linear_check_kernel, dim3(1), kThreads, 0, s, a) != cudaSuccess) return STREE_ERR_CUDA;
     const cudaError_t e = dtype == STREE_BF16 ? launch_prompt<__nv_bfloat16>(a, s) : launch_prompt<float>(a, s);
     return e == cudaSuccess ? STREE_OK : STREE_ERR_CUDA;
 }

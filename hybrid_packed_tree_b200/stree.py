@@ -374,46 +374,67 @@ def stree_tree_attention(q, k_ctx, v_ctx, k_tree, v_tree, ctx_len, parent, o, sc
 
 
 # ---------------------------------------------------------------- prompts, single tokens, the paged cache
+#
+# A decode step makes several of these calls per layer and token, so their checks are one
+# comparison per property and their pointers plain integers: a call costs the host little more
+# than the launch itself.
 
-_F32, _BF16 = (torch.float32,), (torch.bfloat16,)
-_I32, _U8 = (torch.int32,), (torch.uint8,)
+_F32, _BF16, _I32, _U8, _E4M3 = torch.float32, torch.bfloat16, torch.int32, torch.uint8, torch.float8_e4m3fn
+_IO = {torch.float32: STREE_F32, torch.bfloat16: STREE_BF16}
 
 
-def _want(t, name, shape, like):
-    """Shape and device of an argument of the calls below (None passes)."""
-    if t is None:
-        return
+def _refuse(t, name, shape, dtype, dev):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _call(where, fn, like, stream, *args):
-    """Calls a library function on the device of `like`, on its current stream when none is given."""
-    if like.device.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(stream)), where)
-        return
-    with torch.cuda.device(like.device):
-        _check(fn(*args, _stream(stream)), where)
+def _arg(t, name, shape, dtype, dev):
+    """The pointer of a tensor of exactly this shape and dtype, contiguous, on CUDA device `dev`."""
+    try:
+        if t.shape == shape and t.dtype is dtype and t.get_device() == dev and dev >= 0 and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, name, shape, dtype, dev)
 
 
-def _scratch(workspace, like):
+def _opt(t, name, shape, dtype, dev):
+    return None if t is None else _arg(t, name, shape, dtype, dev)
+
+
+def _call(where, fn, dev, stream, *args):
+    """Calls a library function on device `dev`, on that device's current stream when none is given."""
+    if dev == torch._C._cuda_getDevice():
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+    if st != STREE_OK:
+        raise StreeError(st, where)
+
+
+def _scratch(workspace, dev):
     if workspace is None:
         return None, 0
-    if not isinstance(workspace, torch.Tensor) or workspace.device != like.device:
-        raise ValueError(f"workspace must be a tensor on {like.device}")
-    return _ptr(workspace, "workspace", _U8), workspace.numel()
+    n = workspace.numel()
+    return _arg(workspace, "workspace", workspace.shape, _U8, dev), n
 
 
 def stree_linear_prompt_workspace_size(batch, total, heads_v, heads_k, dk, dv, dtype=torch.bfloat16) -> int:
     """Bytes of the workspace in which stree_linear_prompt splits long sequences on the current device (0: no split)."""
     n = ctypes.c_size_t(0)
-    code = {torch.float32: STREE_F32, torch.bfloat16: STREE_BF16}.get(dtype, -1)
     _check(_lib.stree_linear_prompt_workspace_size(int(batch), int(total), int(heads_v), int(heads_k), int(dk), int(dv),
-                                                   code, ctypes.byref(n)), "stree_linear_prompt_workspace_size")
+                                                   _IO.get(dtype, -1), ctypes.byref(n)),
+           "stree_linear_prompt_workspace_size")
     return int(n.value)
 
 
@@ -425,20 +446,16 @@ def stree_linear_prompt(q, k, v, alpha, beta, cu_seqlens, o, S0=None, S_new=None
     skip [Hv] fp32 or None; cu_seqlens [b + 1] int32.  workspace: a device uint8 tensor of
     stree_linear_prompt_workspace_size() bytes, or None (long sequences are not split)."""
     total, Hk, dk = k.shape
-    Hv, dv = v.shape[1], v.shape[2]
-    batch = cu_seqlens.shape[0] - 1
-    _want(cu_seqlens, "cu_seqlens", (batch + 1,), v)
-    for t, name, shape in ((q, "q", (total, Hk, dk)), (k, "k", (total, Hk, dk)), (v, "v", (total, Hv, dv)),
-                           (o, "o", (total, Hv, dv)), (alpha, "alpha", (total, Hv)), (beta, "beta", (total, Hv)),
-                           (S0, "S0", (batch, Hv, dv, dk)), (S_new, "S_new", (batch, Hv, dv, dk)), (skip, "skip", (Hv,)),
-                           (err_out, "err_out", (4,))):
-        _want(t, name, shape, v)
-    io = (v.dtype,)
-    ws, ws_bytes = _scratch(workspace, v)
-    _call("stree_linear_prompt", _lib.stree_linear_prompt, v, stream, _ptr(q, "q", io), _ptr(k, "k", io),
-          _ptr(v, "v", _F32 + _BF16), _ptr(alpha, "alpha", _F32), _ptr(beta, "beta", _F32), _ptr(skip, "skip", _F32),
-          _ptr(S0, "S0", _F32), _ptr(cu_seqlens, "cu_seqlens", _I32), total, batch, Hv, Hk, dk, dv, _io_dtype(v),
-          _ptr(o, "o", io), _ptr(S_new, "S_new", _F32), ws, ws_bytes, _ptr(err_out, "err_out", _I32))
+    _, Hv, dv = v.shape
+    batch, io, dev = cu_seqlens.shape[0] - 1, v.dtype, v.get_device()
+    rows, keys, gates, state = (total, Hv, dv), (total, Hk, dk), (total, Hv), (batch, Hv, dv, dk)
+    ws, ws_bytes = _scratch(workspace, dev)
+    _call("stree_linear_prompt", _lib.stree_linear_prompt, dev, stream, _arg(q, "q", keys, io, dev),
+          _arg(k, "k", keys, io, dev), _arg(v, "v", rows, io, dev), _arg(alpha, "alpha", gates, _F32, dev),
+          _opt(beta, "beta", gates, _F32, dev), _opt(skip, "skip", (Hv,), _F32, dev), _opt(S0, "S0", state, _F32, dev),
+          _arg(cu_seqlens, "cu_seqlens", (batch + 1,), _I32, dev), total, batch, Hv, Hk, dk, dv, _IO.get(io, -1),
+          _arg(o, "o", rows, io, dev), _opt(S_new, "S_new", state, _F32, dev), ws, ws_bytes,
+          _opt(err_out, "err_out", (4,), _I32, dev))
     return o, S_new
 
 
@@ -446,15 +463,13 @@ def stree_linear_step(q, k, v, alpha, beta, S0, o, S_new, skip=None, stream=None
     """One token of stree_linear_prompt's recurrence for every sequence: (o [b, Hv, dv], S_new) from
     q, k [b, Hk, dk], v [b, Hv, dv], alpha, beta [b, Hv] (beta None: ones) and S0 (S_new may be S0)."""
     batch, Hk, dk = k.shape
-    Hv, dv = v.shape[1], v.shape[2]
-    for t, name, shape in ((q, "q", (batch, Hk, dk)), (k, "k", (batch, Hk, dk)), (v, "v", (batch, Hv, dv)),
-                           (o, "o", (batch, Hv, dv)), (alpha, "alpha", (batch, Hv)), (beta, "beta", (batch, Hv)),
-                           (S0, "S0", (batch, Hv, dv, dk)), (S_new, "S_new", (batch, Hv, dv, dk)), (skip, "skip", (Hv,))):
-        _want(t, name, shape, v)
-    io = (v.dtype,)
-    _call("stree_linear_step", _lib.stree_linear_step, v, stream, _ptr(q, "q", io), _ptr(k, "k", io),
-          _ptr(v, "v", _F32 + _BF16), _ptr(alpha, "alpha", _F32), _ptr(beta, "beta", _F32), _ptr(skip, "skip", _F32),
-          _ptr(S0, "S0", _F32), batch, Hv, Hk, dk, dv, _io_dtype(v), _ptr(o, "o", io), _ptr(S_new, "S_new", _F32))
+    _, Hv, dv = v.shape
+    io, dev = v.dtype, v.get_device()
+    rows, keys, gates, state = (batch, Hv, dv), (batch, Hk, dk), (batch, Hv), (batch, Hv, dv, dk)
+    _call("stree_linear_step", _lib.stree_linear_step, dev, stream, _arg(q, "q", keys, io, dev),
+          _arg(k, "k", keys, io, dev), _arg(v, "v", rows, io, dev), _arg(alpha, "alpha", gates, _F32, dev),
+          _opt(beta, "beta", gates, _F32, dev), _opt(skip, "skip", (Hv,), _F32, dev), _arg(S0, "S0", state, _F32, dev),
+          batch, Hv, Hk, dk, dv, _IO.get(io, -1), _arg(o, "o", rows, io, dev), _arg(S_new, "S_new", state, _F32, dev))
     return o, S_new
 
 
@@ -463,32 +478,34 @@ def stree_prompt_attention(q, k, v, cu_seqlens, o, scale, err_out=None, stream=N
     cu_seqlens [b + 1] int32."""
     total, Hq, d = q.shape
     Hkv = k.shape[1]
-    batch = cu_seqlens.shape[0] - 1
-    for t, name, shape in ((q, "q", (total, Hq, d)), (k, "k", (total, Hkv, d)), (v, "v", (total, Hkv, d)),
-                           (o, "o", (total, Hq, d)), (cu_seqlens, "cu_seqlens", (batch + 1,)), (err_out, "err_out", (4,))):
-        _want(t, name, shape, q)
-    _call("stree_prompt_attention", _lib.stree_prompt_attention, q, stream, _ptr(q, "q", _BF16), _ptr(k, "k", _BF16),
-          _ptr(v, "v", _BF16), _ptr(cu_seqlens, "cu_seqlens", _I32), total, batch, Hq, Hkv, d, float(scale), STREE_BF16,
-          _ptr(o, "o", _BF16), _ptr(err_out, "err_out", _I32))
+    batch, dev = cu_seqlens.shape[0] - 1, q.get_device()
+    rows, keys = (total, Hq, d), (total, Hkv, d)
+    _call("stree_prompt_attention", _lib.stree_prompt_attention, dev, stream, _arg(q, "q", rows, _BF16, dev),
+          _arg(k, "k", keys, _BF16, dev), _arg(v, "v", keys, _BF16, dev),
+          _arg(cu_seqlens, "cu_seqlens", (batch + 1,), _I32, dev), total, batch, Hq, Hkv, d, scale, STREE_BF16,
+          _arg(o, "o", rows, _BF16, dev), _opt(err_out, "err_out", (4,), _I32, dev))
     return o
 
 
-def _cache(k_pages, v_pages, page_table, k_scales, v_scales, like):
-    """Pointers and sizes of a paged cache: (k, v, k scales, v scales, table), (n_pages, page size,
-    pages per sequence), its dtype code, heads and head dim."""
-    n_pages, Hkv, page, d = k_pages.shape
-    batch, max_pages = page_table.shape
-    for t, name, shape in ((k_pages, "k_pages", (n_pages, Hkv, page, d)), (v_pages, "v_pages", (n_pages, Hkv, page, d)),
-                           (page_table, "page_table", (batch, max_pages)), (k_scales, "k_scales", (n_pages, Hkv, page)),
-                           (v_scales, "v_scales", (n_pages, Hkv, page))):
-        _want(t, name, shape, like)
-    e4m3 = k_pages.dtype == torch.float8_e4m3fn
-    pages = (torch.float8_e4m3fn,) if e4m3 else _BF16
-    if e4m3 != (k_scales is not None) or e4m3 != (v_scales is not None):
+def _cache(k_pages, v_pages, page_table, k_scales, v_scales, batch, dev):
+    """Pointers and sizes of a paged cache: (k, v, k scales, v scales, table), (heads, head dim, n_pages,
+    page size, pages per sequence), its dtype code."""
+    shape, pages = k_pages.shape, k_pages.dtype
+    if len(shape) != 4 or page_table.dim() != 2:
+        raise ValueError("k_pages is [n_pages, Hkv, page_size, 128] and page_table [batch, max_pages]")
+    n_pages, Hkv, page, d = shape
+    max_pages = page_table.shape[1]
+    code = STREE_BF16
+    if pages is _E4M3:
+        code = STREE_E4M3
+    elif pages is not _BF16:
+        raise TypeError(f"k_pages has dtype {pages}, expected torch.bfloat16 or torch.float8_e4m3fn")
+    if (k_scales is not None) != (code == STREE_E4M3) or (v_scales is not None) != (code == STREE_E4M3):
         raise ValueError("k_scales and v_scales go with float8_e4m3fn pages, and with them alone")
-    return ((_ptr(k_pages, "k_pages", pages), _ptr(v_pages, "v_pages", pages), _ptr(k_scales, "k_scales", _U8),
-             _ptr(v_scales, "v_scales", _U8), _ptr(page_table, "page_table", _I32)), (n_pages, page, max_pages),
-            STREE_E4M3 if e4m3 else STREE_BF16, Hkv, d)
+    return ((_arg(k_pages, "k_pages", shape, pages, dev), _arg(v_pages, "v_pages", shape, pages, dev),
+             _opt(k_scales, "k_scales", (n_pages, Hkv, page), _U8, dev),
+             _opt(v_scales, "v_scales", (n_pages, Hkv, page), _U8, dev),
+             _arg(page_table, "page_table", (batch, max_pages), _I32, dev)), (Hkv, d, n_pages, page, max_pages), code)
 
 
 def stree_paged_attention_workspace_size(heads_q, heads_kv, head_dim=128) -> int:
@@ -506,14 +523,13 @@ def stree_paged_attention(q, k_pages, v_pages, page_table, seq_len, o, scale, k_
     [b, max_pages] and seq_len [b] int32.  workspace: a device uint8 tensor of
     stree_paged_attention_workspace_size() bytes."""
     batch, Hq, d = q.shape
-    ptrs, sizes, code, Hkv, dc = _cache(k_pages, v_pages, page_table, k_scales, v_scales, q)
-    for t, name, shape in ((q, "q", (batch, Hq, dc)), (o, "o", (batch, Hq, d)), (seq_len, "seq_len", (batch,)),
-                           (page_table, "page_table", (batch, sizes[2])), (err_out, "err_out", (4,))):
-        _want(t, name, shape, q)
-    ws, ws_bytes = _scratch(workspace, q)
-    _call("stree_paged_attention", _lib.stree_paged_attention, q, stream, _ptr(q, "q", _BF16), *ptrs,
-          _ptr(seq_len, "seq_len", _I32), batch, Hq, Hkv, d, *sizes, float(scale), STREE_BF16, code, _ptr(o, "o", _BF16),
-          ws, ws_bytes, _ptr(err_out, "err_out", _I32))
+    dev = q.get_device()
+    ptrs, sizes, code = _cache(k_pages, v_pages, page_table, k_scales, v_scales, batch, dev)
+    rows = (batch, Hq, sizes[1])
+    ws, ws_bytes = _scratch(workspace, dev)
+    _call("stree_paged_attention", _lib.stree_paged_attention, dev, stream, _arg(q, "q", rows, _BF16, dev), *ptrs,
+          _arg(seq_len, "seq_len", (batch,), _I32, dev), batch, Hq, *sizes, scale, STREE_BF16, code,
+          _arg(o, "o", rows, _BF16, dev), ws, ws_bytes, _opt(err_out, "err_out", (4,), _I32, dev))
     return o
 
 
@@ -522,14 +538,13 @@ def stree_cache_write(k, v, cu_seqlens, start, page_table, k_pages, v_pages, k_s
     """Writes packed new keys and values k, v [total, Hkv, 128] (bf16) into the pages, token i of
     sequence b at position start[b] + i; quantised as they are written when the pages are
     float8_e4m3fn (one power-of-two scale per row, in k_scales and v_scales)."""
-    ptrs, sizes, code, Hkv, d = _cache(k_pages, v_pages, page_table, k_scales, v_scales, k)
-    total, batch = k.shape[0], page_table.shape[0]
-    for t, name, shape in ((k, "k", (total, Hkv, d)), (v, "v", (total, Hkv, d)), (cu_seqlens, "cu_seqlens", (batch + 1,)),
-                           (start, "start", (batch,)), (err_out, "err_out", (4,))):
-        _want(t, name, shape, k)
-    _call("stree_cache_write", _lib.stree_cache_write, k, stream, _ptr(k, "k", _BF16), _ptr(v, "v", _BF16),
-          _ptr(cu_seqlens, "cu_seqlens", _I32), _ptr(start, "start", _I32), ptrs[4], total, batch, Hkv, d, *sizes,
-          STREE_BF16, code, *ptrs[:4], _ptr(err_out, "err_out", _I32))
+    total, batch, dev = k.shape[0], start.shape[0], k.get_device()
+    ptrs, sizes, code = _cache(k_pages, v_pages, page_table, k_scales, v_scales, batch, dev)
+    rows = (total, sizes[0], sizes[1])
+    _call("stree_cache_write", _lib.stree_cache_write, dev, stream, _arg(k, "k", rows, _BF16, dev),
+          _arg(v, "v", rows, _BF16, dev), _arg(cu_seqlens, "cu_seqlens", (batch + 1,), _I32, dev),
+          _arg(start, "start", (batch,), _I32, dev), ptrs[4], total, batch, *sizes, STREE_BF16, code, *ptrs[:4],
+          _opt(err_out, "err_out", (4,), _I32, dev))
     return k_pages, v_pages
 
 
@@ -537,17 +552,14 @@ def stree_cache_commit(k_tree, v_tree, path, path_len, start, page_table, k_page
                        v_scales=None, err_out=None, stream=None):
     """Writes the accepted path of each tree into the pages: node path[b, i] of k_tree, v_tree
     [b, T, Hkv, 128] (bf16) at position start[b] + i, i < path_len[b]."""
-    ptrs, sizes, code, Hkv, d = _cache(k_pages, v_pages, page_table, k_scales, v_scales, k_tree)
     batch, T = k_tree.shape[:2]
-    maxlen = path.shape[1]
-    for t, name, shape in ((k_tree, "k_tree", (batch, T, Hkv, d)), (v_tree, "v_tree", (batch, T, Hkv, d)),
-                           (path, "path", (batch, maxlen)), (path_len, "path_len", (batch,)), (start, "start", (batch,)),
-                           (page_table, "page_table", (batch, sizes[2])), (err_out, "err_out", (4,))):
-        _want(t, name, shape, k_tree)
-    _call("stree_cache_commit", _lib.stree_cache_commit, k_tree, stream, _ptr(k_tree, "k_tree", _BF16),
-          _ptr(v_tree, "v_tree", _BF16), _ptr(path, "path", _I32), _ptr(path_len, "path_len", _I32), maxlen,
-          _ptr(start, "start", _I32), ptrs[4], T, batch, Hkv, d, *sizes, STREE_BF16, code, *ptrs[:4],
-          _ptr(err_out, "err_out", _I32))
+    maxlen, dev = path.shape[1], k_tree.get_device()
+    ptrs, sizes, code = _cache(k_pages, v_pages, page_table, k_scales, v_scales, batch, dev)
+    rows = (batch, T, sizes[0], sizes[1])
+    _call("stree_cache_commit", _lib.stree_cache_commit, dev, stream, _arg(k_tree, "k_tree", rows, _BF16, dev),
+          _arg(v_tree, "v_tree", rows, _BF16, dev), _arg(path, "path", (batch, maxlen), _I32, dev),
+          _arg(path_len, "path_len", (batch,), _I32, dev), maxlen, _arg(start, "start", (batch,), _I32, dev), ptrs[4], T,
+          batch, *sizes, STREE_BF16, code, *ptrs[:4], _opt(err_out, "err_out", (4,), _I32, dev))
     return k_pages, v_pages
 
 
@@ -555,15 +567,14 @@ def stree_cache_read(k_pages, v_pages, page_table, seq_len, k_ctx, v_ctx, k_scal
                      stream=None):
     """Reads the first seq_len[b] positions of the pages back into the contiguous cache of
     stree_tree_attention, k_ctx, v_ctx [b, S, Hkv, 128] (bf16); later positions are untouched."""
-    ptrs, sizes, code, Hkv, d = _cache(k_pages, v_pages, page_table, k_scales, v_scales, k_ctx)
     batch, S = k_ctx.shape[:2]
-    for t, name, shape in ((k_ctx, "k_ctx", (batch, S, Hkv, d)), (v_ctx, "v_ctx", (batch, S, Hkv, d)),
-                           (seq_len, "seq_len", (batch,)), (page_table, "page_table", (batch, sizes[2])),
-                           (err_out, "err_out", (4,))):
-        _want(t, name, shape, k_ctx)
-    _call("stree_cache_read", _lib.stree_cache_read, k_ctx, stream, *ptrs, _ptr(seq_len, "seq_len", _I32), batch, S, Hkv,
-          d, *sizes, code, STREE_BF16, _ptr(k_ctx, "k_ctx", _BF16), _ptr(v_ctx, "v_ctx", _BF16),
-          _ptr(err_out, "err_out", _I32))
+    dev = k_ctx.get_device()
+    ptrs, sizes, code = _cache(k_pages, v_pages, page_table, k_scales, v_scales, batch, dev)
+    rows = (batch, S, sizes[0], sizes[1])
+    _call("stree_cache_read", _lib.stree_cache_read, dev, stream, *ptrs,
+          _arg(seq_len, "seq_len", (batch,), _I32, dev), batch, S, *sizes, code, STREE_BF16,
+          _arg(k_ctx, "k_ctx", rows, _BF16, dev), _arg(v_ctx, "v_ctx", rows, _BF16, dev),
+          _opt(err_out, "err_out", (4,), _I32, dev))
     return k_ctx, v_ctx
 
 

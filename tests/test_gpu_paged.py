@@ -317,3 +317,30 @@ def test_cache_read_skips_pages_out_of_range(st):
     assert err.tolist() == [10, 0, 1, BAD]
     assert torch.all(kc[0, :8] == 3) and torch.all(kc[0, 8:16] == 7) and torch.all(vc[0, 16:] == 3)
     assert torch.all(kc[1, :9] == 3) and torch.all(vc[1, 9:] == 7)
+
+
+def test_binding_refuses_each_tensor(st):
+    """Every tensor of a call in a wrong shape, dtype, order of memory or place."""
+    rng = np.random.default_rng(10)
+    a = _cache(rng, [20, 30], 2, 8, "e4m3")
+    q = bf16(rng.normal(size=(2, 8, 128)))
+    ws = torch.empty(st.stree_paged_attention_workspace_size(8, 2), dtype=torch.uint8, device="cuda")
+    good = dict(q=q, k_pages=a["k_pages"], v_pages=a["v_pages"], page_table=a["table"], seq_len=a["lens"],
+                o=torch.empty_like(q), scale=SCALE, k_scales=a["k_scales"], v_scales=a["v_scales"],
+                err_out=torch.zeros(4, dtype=torch.int32, device="cuda"), workspace=ws)
+    st.stree_paged_attention(**good)
+    for name, t in good.items():
+        if name == "scale":
+            continue
+        wrong = [t.cpu(), t.double() if t.dtype is not torch.float8_e4m3fn else t.view(torch.uint8)]
+        if name not in ("workspace",):
+            wrong.append(t[:-1])
+        if t.dim() > 1:
+            wrong.append(t.transpose(0, 1).contiguous().transpose(0, 1))
+        for w in wrong:
+            with pytest.raises((ValueError, TypeError)):
+                st.stree_paged_attention(**{**good, name: w})
+    with pytest.raises(ValueError):            # a key head count that the queries do not have
+        st.stree_paged_attention(**{**good, "v_pages": a["v_pages"][:, :1].contiguous()})
+    with pytest.raises(st.StreeError):
+        st.stree_paged_attention(**{**good, "q": q[:, :7].contiguous(), "o": q[:, :7].contiguous()})

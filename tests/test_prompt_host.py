@@ -118,22 +118,29 @@ def test_cache_calls(lib):
     assert _call(lib.stree_cache_read, read, i6=0) == 0
 
 
-def test_binding_checks_shapes_before_pointers(lib):
+def test_binding_refuses_on_the_host(lib):
+    """No call reaches the library with tensors of other shapes, dtypes or devices."""
     from hybrid_packed_tree_b200 import stree
     bf = dict(dtype=torch.bfloat16)
     q, k = torch.zeros(5, 4, 128, **bf), torch.zeros(5, 2, 128, **bf)
     cu = torch.zeros(3, dtype=torch.int32)
-    with pytest.raises(ValueError, match="v has shape"):
-        stree.stree_prompt_attention(q, k, k[:4], cu, q, 0.1)
-    with pytest.raises(ValueError, match="alpha has shape"):
-        stree.stree_linear_prompt(k, k, q, torch.zeros(5, 3), None, cu, q)
-    with pytest.raises(ValueError, match="S0 has shape"):
-        stree.stree_linear_step(k, k, q, torch.zeros(5, 4), None, torch.zeros(5, 4, 128, 64), q, torch.zeros(5, 4, 128, 128))
+    with pytest.raises(ValueError, match="q must be a CUDA tensor"):
+        stree.stree_prompt_attention(q, k, k, cu, q, 0.1)
+    with pytest.raises(ValueError, match="q has shape"):
+        stree.stree_linear_prompt(k[:4], k, q, torch.zeros(5, 4), None, cu, q)
+    with pytest.raises(TypeError, match="q has dtype"):
+        stree.stree_linear_step(k.float(), k, q, torch.zeros(5, 4), None, torch.zeros(5, 4, 128, 128), q, torch.zeros(5, 4, 128, 128))
+    with pytest.raises(TypeError, match="q must be a torch.Tensor"):
+        stree.stree_linear_prompt(None, k, q, torch.zeros(5, 4), None, cu, q)
     pages = torch.zeros(3, 2, 16, 128, **bf)
     table = torch.zeros(2, 4, dtype=torch.int32)
-    with pytest.raises(ValueError, match="v_pages has shape"):
-        stree.stree_cache_write(k, k, cu, table[:, 0], table, pages, pages[:2])
+    with pytest.raises(ValueError, match="k_pages must be a CUDA tensor"):
+        stree.stree_cache_write(k, k, cu, table[:, 0], table, pages, pages)
     with pytest.raises(ValueError, match="go with float8"):
         stree.stree_cache_write(k, k, cu, table[:, 0], table, pages, pages, k_scales=torch.zeros(3, 2, 16, dtype=torch.uint8))
-    with pytest.raises(ValueError, match="must be a CUDA tensor"):
-        stree.stree_paged_attention(q[:2], pages, pages, table, cu[:2], q[:2], 0.1)
+    with pytest.raises(ValueError, match="go with float8"):
+        stree.stree_cache_read(pages.to(torch.float8_e4m3fn), pages, table, cu[:2], pages[:2], pages[:2])
+    with pytest.raises(TypeError, match="expected torch.bfloat16 or torch.float8_e4m3fn"):
+        stree.stree_paged_attention(q[:2], pages.float(), pages, table, cu[:2], q[:2], 0.1)
+    with pytest.raises(ValueError, match="page_table"):
+        stree.stree_paged_attention(q[:2], pages, pages, table[0], cu[:2], q[:2], 0.1)
