@@ -23,8 +23,12 @@
 // most one eighth full and adds a round trip through tensor memory for each block.
 // 8-bit pages: keys and values become fp16 exactly (every e4m3 is one).  A query row is
 // scaled to [-1, 1] by a power of two so that it is fp16 as well (an element below 2^-14 of
-// the row's largest loses bits that the fp32 sum would not keep either); a key's scale
-// multiplies its score and a value's scale its probability, in fp32.
+// the row's largest loses bits that the fp32 sum would not keep either).  A key's scale
+// multiplies its score; a value's scale 2^e joins its probability before that is rounded to
+// fp16, so the sum has a reference of its own, the maximum of score + e: the largest weight is 1
+// and none overflows, whatever the scales.  (Values widened to bf16 with the scale on a bf16
+// probability took twice the instructions: 120 us against 62 at 64 sequences of up to 4096
+// tokens, where the loads alone would take 42.)
 #include <cuda.h>
 
 #include <mutex>
@@ -56,7 +60,8 @@ struct PagedArgs {
     const int32_t *table, *lens;
     __nv_bfloat16 *o;
     float *part_o;                             // [share][2][rows][128]
-    float2 *part_ml;                           // [share][2][rows]: (reference, sum); sum < 0: bad page
+    float4 *part_ml;                           // [share][2][rows]: (output's reference, sum's reference, sum,
+                                               // nonzero: a page out of range)
     int32_t *err;
     int batch, heads_q, heads_kv, group, row_tiles, rows;   // rows: min(group, 16)
     int n_pages, page_size, max_pages, box_rows, shares, stages;
@@ -106,12 +111,20 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// Two e4m3 -> two bf16, exactly.
-__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t w)
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi)
 {
-    const uint32_t h = e4m3x2_to_f16x2(w);
-    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-    return pack_bf16(f.x, f.y);
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// Joins partial results (output's reference, sum's reference, sum) whose outputs and sums are
+// x = 2^-reference (unnormalised output) and likewise the sum.
+__device__ __forceinline__ float weight(float ref, float top) { return ref == -INFINITY ? 0.f : ptx::ex2_approx(ref - top); }
+
+// Output over sum, given both references.
+__device__ __forceinline__ float quotient(float x, float ref, float m, float sum)
+{
+    return sum > 0.f ? x * ptx::ex2_approx(ref - m) / sum : x;
 }
 
 struct Stage {                                 // offsets inside a stage of the ring
@@ -135,7 +148,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
     __shared__ uint64_t bars[2 * kMaxStages];
     __shared__ int tmp[33], found[2];
     __shared__ volatile int aborted, bad[kMaxStages];
-    __shared__ float2 ml_s[kComputeWarps][kHeadRows];
+    __shared__ float4 ml_s[kComputeWarps][kHeadRows];
     uint8_t *smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
     float *joined = reinterpret_cast<float *>(smem + a.stages * L.bytes);   // [4][rows][128]
     auto full = [&](int s) { return ptx::smem_u32(&bars[s]); };
@@ -187,13 +200,6 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
     }
     __syncthreads();
 
-    auto wait = [&](uint32_t bar, uint32_t parity, int where) -> bool {
-        if (aborted) return false;
-        if (ptx::mbar_wait(bar, parity)) return true;
-        if (a.err) latch_error(a.err, STREE_ERR_TIMEOUT, b_first, where, (int)parity);
-        aborted = 1;
-        return false;
-    };
     // Where the share begins: its sequence, row of blocks (item) and block.
     int b = b_first, nb = blocks_of(a, b);
     long long left = end - begin;
@@ -215,74 +221,91 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
             ptx::prefetch_tensormap(&tm_k);
             ptx::prefetch_tensormap(&tm_v);
         }
-        // Lane i < 8 looks up the page of positions 8 i .. 8 i + 7 (an eighth lies in one page).
-        auto lookup = [&](int bb, int bl) -> int {
-            const int pos = bl * kBlk + (lane & 7) * 8;
-            const int n = min(max(__ldg(a.lens + bb), 0), a.max_pages * a.page_size);
-            if (pos >= n) return -2;           // nothing there
-            const int id = __ldg(a.table + (size_t)bb * a.max_pages + pos / a.page_size);
-            return id >= 0 && id < a.n_pages ? id : -1;
+        // Lane i (mod 8) follows positions 8 i .. 8 i + 7 of the block (an eighth lies in one page): their
+        // page's place in the table and row in the page, moved on by 64 positions without a
+        // division (the page ids of one block ahead are in flight while a block is issued).
+        const int mine8 = (lane & 7) * 8, step_p = kBlk / a.page_size, step_r = kBlk % a.page_size;
+        const int first_p = mine8 / a.page_size, first_r = mine8 % a.page_size;
+        int at_p = (blk * kBlk + mine8) / a.page_size, at_r = (blk * kBlk + mine8) % a.page_size;
+        int n = min(max(__ldg(a.lens + b), 0), a.max_pages * a.page_size);
+        int row0 = a.row_tiles == 1 ? item : item / a.row_tiles;   // key/value head
+        auto lookup = [&]() -> int {
+            if (blk * kBlk + mine8 >= n) return -2;   // nothing there
+            return __ldg(a.table + (size_t)b * a.max_pages + at_p);
         };
-        int id = lookup(b, blk);
-        uint64_t issued = 0;
+        int id = lookup(), stage = 0, issued = 0;
+        uint32_t lap = 0;                      // how often the ring has been filled
+#pragma unroll 1
         for (; left > 0; --left, ++issued) {
-            const int s = (int)(issued % a.stages);
-            const int cb = b, citem = item, cblk = blk, cid = id;
+            const int chead = row0, crow = at_r;
+            const int cid = id == -2 || (id >= 0 && id < a.n_pages) ? id : -1;
             if (left > 1) {
+                const int was_b = b, was_item = item;
                 advance();
-                id = lookup(b, blk);
+                if (b != was_b || item != was_item) {
+                    at_p = first_p;
+                    at_r = first_r;
+                    row0 = a.row_tiles == 1 ? item : item / a.row_tiles;
+                    if (b != was_b) n = min(max(__ldg(a.lens + b), 0), a.max_pages * a.page_size);
+                } else {
+                    at_p += step_p;
+                    at_r += step_r;
+                    if (at_r >= a.page_size) {
+                        at_r -= a.page_size;
+                        ++at_p;
+                    }
+                }
+                id = lookup();
             }
-            bool ok = true;
-            if (issued >= (uint64_t)a.stages) {
-                if (lane == 0) ok = wait(empty(s), (uint32_t)((issued / a.stages - 1) & 1), 1);
-                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-            }
-            if (!ok) break;
-            const int hkv = citem / a.row_tiles;
-            const int eighth = lane * (a.box_rows / 8);   // of the box that this lane issues
-            const int box_id = __shfl_sync(0xffffffffu, cid, eighth & 7);
+            if (lap > 0 && !wait_warp(&aborted, empty(stage), lap - 1, 1)) break;
+            const int eighth = (lane * (a.box_rows / 8)) & 7;   // of the box that this lane issues
+            const int box_id = __shfl_sync(0xffffffffu, cid, eighth), box_row = __shfl_sync(0xffffffffu, crow, eighth);
             const bool mine = lane < boxes && box_id >= 0;
             const uint32_t n_boxes = __popc(__ballot_sync(0xffffffffu, mine));
             const bool any_bad = __any_sync(0xffffffffu, cid == -1);
-            const uint32_t base = ptx::smem_u32(smem + s * L.bytes);
+            const uint32_t base = ptx::smem_u32(smem) + stage * L.bytes, fb = full(stage);
             if (lane == 0) {
-                bad[s] = any_bad;
-                ptx::mbar_expect_tx(full(s), n_boxes * box_bytes * (kE4m3 ? 2u : 4u));
+                bad[stage] = any_bad;
+                ptx::mbar_expect_tx(fb, n_boxes * box_bytes * (kE4m3 ? 2u : 4u));
             }
             __syncwarp();
             if (mine) {
-                const int pos = cblk * kBlk + lane * a.box_rows;
-                const int row = (box_id * a.heads_kv + hkv) * a.page_size + pos % a.page_size;
+                const int row = (box_id * a.heads_kv + chead) * a.page_size + box_row;
                 const uint32_t at = base + (uint32_t)lane * box_bytes;
-                ptx::tma_load_2d(at + L.k, &tm_k, 0, row, full(s));
-                ptx::tma_load_2d(at + L.v, &tm_v, 0, row, full(s));
+                ptx::tma_load_2d(at + L.k, &tm_k, 0, row, fb);
+                ptx::tma_load_2d(at + L.v, &tm_v, 0, row, fb);
                 if (!kE4m3) {
-                    ptx::tma_load_2d(at + L.k + 8192, &tm_k, 64, row, full(s));
-                    ptx::tma_load_2d(at + L.v + 8192, &tm_v, 64, row, full(s));
+                    ptx::tma_load_2d(at + L.k + 8192, &tm_k, 64, row, fb);
+                    ptx::tma_load_2d(at + L.v + 8192, &tm_v, 64, row, fb);
                 }
             }
             if (kE4m3 && lane < 16) {
                 // Lanes 0-7 the eighths of the key scales, 8-15 of the value scales.
-                if (cid >= 0) {
-                    const size_t at = ((size_t)cid * a.heads_kv + hkv) * a.page_size + (cblk * kBlk + (lane & 7) * 8) % a.page_size;
-                    ptx::cp_async8(base + (lane < 8 ? L.ks : L.vs) + (lane & 7) * 8, (lane < 8 ? a.k_scales : a.v_scales) + at);
-                }
-                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full(s)) : "memory");
+                if (cid >= 0)
+                    ptx::cp_async8(base + (lane < 8 ? L.ks : L.vs) + mine8,
+                                   (lane < 8 ? a.k_scales : a.v_scales) + ((size_t)cid * a.heads_kv + chead) * a.page_size + crow);
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(fb) : "memory");
+            }
+            if (++stage == a.stages) {
+                stage = 0;
+                ++lap;
             }
         }
         // Nothing may still be landing in shared memory when the CTA ends.
         if (aborted) {
+            if (lane == 0 && a.err) latch_error(a.err, STREE_ERR_TIMEOUT, b_first, aborted, 0);
             if (kE4m3) ptx::cp_async_wait_all();
             if (lane == 0)
-                for (uint64_t i = issued > (uint64_t)a.stages ? issued - a.stages : 0; i < issued; ++i)
-                    ptx::mbar_wait(full((int)(i % a.stages)), (uint32_t)((i / a.stages) & 1));
+                for (int i = max(0, issued - a.stages); i < issued; ++i)
+                    ptx::mbar_wait(full(i % a.stages), (uint32_t)((i / a.stages) & 1));
         }
         return;
     }
 
     // ---------------------------------------------------------------- compute
     const int t4 = lane & 3, r4 = lane >> 2;
-    uint64_t taken = 0;
+    int s = 0;                                 // the stage, and its use's number
+    uint32_t phase = 0;
     bool run = true;
     int piece = 0;                             // 0: the share's first row of blocks, 1: a later one
     while (left > 0 && run) {
@@ -336,13 +359,10 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
         for (int i = 0; i < 16; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        float m[2] = {-INFINITY, -INFINITY}, ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
         int any_bad = 0;
         while (true) {
-            const int s = (int)(taken % a.stages);
-            if (lane == 0) run = wait(full(s), (uint32_t)((taken / a.stages) & 1), 10);
-            run = __shfl_sync(0xffffffffu, run ? 1 : 0, 0) != 0;
-            if (!run) break;
+            if (!(run = wait_warp(&aborted, full(s), phase, 10))) break;
             any_bad |= bad[s];
             const uint32_t base = ptx::smem_u32(smem + s * L.bytes);
             const int key0 = warp * 16, valid = n - (blk * kBlk + key0);   // positions of this warp that exist
@@ -373,37 +393,54 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
                     }
                 }
                 // This thread's scores: rows r4 and r4 + 8, positions key0 + 8 j + 2 t4 + {0, 1}.
-                float vscale[4] = {1.f, 1.f, 1.f, 1.f};
+                const bool tail = valid < 16;
+                float ve[4] = {0.f, 0.f, 0.f, 0.f};   // log2 of the values' scales
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int key = 8 * j + 2 * t4 + e;
-                        float ks = 1.f;
-                        if (kE4m3) {
-                            const uint8_t *sb = smem + s * L.bytes;
-                            ks = power_of_two(sb[L.ks + key0 + key]);
-                            // Past the end the byte may be anything, and 0 x infinity is NaN.
-                            vscale[2 * j + e] = key < valid ? power_of_two(sb[L.vs + key0 + key]) : 0.f;
-                        }
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            sc[j][2 * i + e] = key < valid ? sc[j][2 * i + e] * (kE4m3 ? qs[i] * ks : qs[i]) : -INFINITY;
+                for (int j = 0; j < 2; ++j) {
+                    float f[2][2] = {{qs[0], qs[0]}, {qs[1], qs[1]}};
+                    if (kE4m3) {
+                        const uint8_t *sb = smem + s * L.bytes + key0 + 8 * j + 2 * t4;
+                        const uint32_t kb = *reinterpret_cast<const uint16_t *>(sb + L.ks), vb = *reinterpret_cast<const uint16_t *>(sb + L.vs);
+                        const float k0 = power_of_two(kb & 0xffu), k1 = power_of_two(kb >> 8);
+                        ve[2 * j] = __uint_as_float(0x4b000000u | (vb & 0xffu)) - 8388735.f;   // 2^23 + byte, less 2^23 + 127
+                        ve[2 * j + 1] = __uint_as_float(0x4b000000u | (vb >> 8)) - 8388735.f;
+                        f[0][0] *= k0;
+                        f[0][1] *= k1;
+                        f[1][0] *= k0;
+                        f[1][1] *= k1;
                     }
-                float mn[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) sc[j][2 * i + e] *= f[i][e];
+                }
+                if (tail)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (8 * j + 2 * t4 + (e & 1) >= valid) sc[j][e] = -INFINITY;
+                // Running maxima of the scores and, for the output, of the scores with the values' scales.
+                float mn[2], rn[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     mn[i] = fmaxf(fmaxf(sc[0][2 * i], sc[0][2 * i + 1]), fmaxf(sc[1][2 * i], sc[1][2 * i + 1]));
                     mn[i] = fmaxf(mn[i], __shfl_xor_sync(0xffffffffu, mn[i], 1));
-                    mn[i] = fmaxf(mn[i], __shfl_xor_sync(0xffffffffu, mn[i], 2));
-                    mn[i] = fmaxf(mn[i], m[i]);
+                    mn[i] = fmaxf(m[i], fmaxf(mn[i], __shfl_xor_sync(0xffffffffu, mn[i], 2)));
+                    rn[i] = mn[i];
+                    if (kE4m3) {
+                        rn[i] = fmaxf(fmaxf(sc[0][2 * i] + ve[0], sc[0][2 * i + 1] + ve[1]), fmaxf(sc[1][2 * i] + ve[2], sc[1][2 * i + 1] + ve[3]));
+                        rn[i] = fmaxf(rn[i], __shfl_xor_sync(0xffffffffu, rn[i], 1));
+                        rn[i] = fmaxf(ref[i], fmaxf(rn[i], __shfl_xor_sync(0xffffffffu, rn[i], 2)));
+                    }
                 }
-                if (__any_sync(0xffffffffu, mn[0] > m[0] || mn[1] > m[1])) {
+                if (__any_sync(0xffffffffu, mn[0] > m[0] || mn[1] > m[1] || rn[0] > ref[0] || rn[1] > ref[1])) {
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const float f = mn[i] == m[i] ? 1.f : ptx::ex2_approx(m[i] - mn[i]);
-                        l[i] *= f;
+                        const float f = rn[i] == ref[i] ? 1.f : ptx::ex2_approx(ref[i] - rn[i]);
+                        l[i] *= mn[i] == m[i] ? 1.f : ptx::ex2_approx(m[i] - mn[i]);
                         m[i] = mn[i];
+                        ref[i] = rn[i];
 #pragma unroll
                         for (int c = 0; c < 16; ++c) {
                             acc[c][2 * i] *= f;
@@ -413,14 +450,17 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
                 }
                 uint32_t pf[4];
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int i = 0; i < 2; ++i) {
+                    const float mi = m[i] == -INFINITY ? 0.f : m[i], ri = ref[i] == -INFINITY ? 0.f : ref[i];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float ref = m[i] == -INFINITY ? 0.f : m[i];
-                        const float p0 = ptx::ex2_approx(sc[j][2 * i] - ref), p1 = ptx::ex2_approx(sc[j][2 * i + 1] - ref);
+                    for (int j = 0; j < 2; ++j) {
+                        const float p0 = ptx::ex2_approx(sc[j][2 * i] - mi), p1 = ptx::ex2_approx(sc[j][2 * i + 1] - mi);
                         l[i] += p0 + p1;
-                        pf[2 * j + i] = kE4m3 ? pack_bf16(p0 * vscale[2 * j], p1 * vscale[2 * j + 1]) : pack_bf16(p0, p1);
+                        pf[2 * j + i] = kE4m3 ? pack_half(ptx::ex2_approx(sc[j][2 * i] + (ve[2 * j] - ri)),
+                                                          ptx::ex2_approx(sc[j][2 * i + 1] + (ve[2 * j + 1] - ri)))
+                                              : pack_bf16(p0, p1);
                     }
+                }
                 // Positions past the end hold anything: their value rows count as zero.
                 const uint32_t keep0 = (2 * t4 < valid ? 0xffffu : 0u) | (2 * t4 + 1 < valid ? 0xffff0000u : 0u);
                 const uint32_t keep1 = (2 * t4 + 8 < valid ? 0xffffu : 0u) | (2 * t4 + 9 < valid ? 0xffff0000u : 0u);
@@ -436,10 +476,16 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
                             const uint32_t x = __byte_perm(r[2 * j], 0, 0x3120), y = __byte_perm(r[2 * j + 1], 0, 0x3120);
-                            mma16816<false>(acc[2 * (c + j)], pf, e4m3x2_to_bf16x2(x & 0xffffu) & keep0,
-                                            e4m3x2_to_bf16x2(y & 0xffffu) & keep1);
-                            mma16816<false>(acc[2 * (c + j) + 1], pf, e4m3x2_to_bf16x2(x >> 16) & keep0,
-                                            e4m3x2_to_bf16x2(y >> 16) & keep1);
+                            uint32_t v[4] = {e4m3x2_to_f16x2(x & 0xffffu), e4m3x2_to_f16x2(y & 0xffffu), e4m3x2_to_f16x2(x >> 16),
+                                             e4m3x2_to_f16x2(y >> 16)};
+                            if (tail) {
+                                v[0] &= keep0;
+                                v[1] &= keep1;
+                                v[2] &= keep0;
+                                v[3] &= keep1;
+                            }
+                            mma16816<true>(acc[2 * (c + j)], pf, v[0], v[1]);
+                            mma16816<true>(acc[2 * (c + j) + 1], pf, v[2], v[3]);
                         }
                     }
                 } else {
@@ -448,14 +494,23 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
                         uint32_t r[4];
                         const int chunk = 2 * c + (lane >> 4);
                         ldsm4_t(base + L.v + (chunk >> 3) * 8192 + row * 128 + (((chunk & 7) ^ (row & 7)) << 4), r);
-                        mma16816<false>(acc[2 * c], pf, r[0] & keep0, r[1] & keep1);
-                        mma16816<false>(acc[2 * c + 1], pf, r[2] & keep0, r[3] & keep1);
+                        if (tail) {
+                            r[0] &= keep0;
+                            r[1] &= keep1;
+                            r[2] &= keep0;
+                            r[3] &= keep1;
+                        }
+                        mma16816<false>(acc[2 * c], pf, r[0], r[1]);
+                        mma16816<false>(acc[2 * c + 1], pf, r[2], r[3]);
                     }
                 }
             }
             __syncwarp();
             if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(empty(s)) : "memory");
-            ++taken;
+            if (++s == a.stages) {
+                s = 0;
+                ++phase;
+            }
             --left;
             const bool last = left == 0 || blk + 1 == nb;
             if (left > 0) advance();
@@ -468,7 +523,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
             l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
             const int r = r4 + 8 * i;
             if (r >= rows) continue;
-            if (t4 == 0) ml_s[warp][r] = make_float2(m[i], l[i]);
+            if (t4 == 0) ml_s[warp][r] = make_float4(ref[i], m[i], l[i], 0.f);
             float *dst = joined + ((size_t)warp * a.rows + r) * kD;
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
@@ -486,21 +541,23 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
         if (!aborted) {
             const size_t slot = (size_t)blockIdx.x * 2 + piece;
             for (int r = 0; r < rows; ++r) {
-                float M = -INFINITY, den = 0.f, x = 0.f;
-#pragma unroll
-                for (int w = 0; w < kComputeWarps; ++w) M = fmaxf(M, ml_s[w][r].x);
+                float R = -INFINITY, M = -INFINITY, den = 0.f, x = 0.f;
 #pragma unroll
                 for (int w = 0; w < kComputeWarps; ++w) {
-                    const float2 ml = ml_s[w][r];
-                    const float f = ml.x == -INFINITY ? 0.f : ptx::ex2_approx(ml.x - M);
-                    x = fmaf(f, joined[((size_t)w * a.rows + r) * kD + tid], x);
-                    den = fmaf(f, ml.y, den);
+                    R = fmaxf(R, ml_s[w][r].x);
+                    M = fmaxf(M, ml_s[w][r].y);
+                }
+#pragma unroll
+                for (int w = 0; w < kComputeWarps; ++w) {
+                    const float4 ml = ml_s[w][r];
+                    x = fmaf(weight(ml.x, R), joined[((size_t)w * a.rows + r) * kD + tid], x);
+                    den = fmaf(weight(ml.y, M), ml.z, den);
                 }
                 if (!whole) {
                     a.part_o[(slot * a.rows + r) * kD + tid] = x;
-                    if (tid == 0) a.part_ml[slot * a.rows + r] = make_float2(M, any_bad ? -1.f : den);
+                    if (tid == 0) a.part_ml[slot * a.rows + r] = make_float4(R, M, den, any_bad ? 1.f : 0.f);
                 } else if (!any_bad) {
-                    a.o[((size_t)cb * a.heads_q + head0 + r) * kD + tid] = __float2bfloat16_rn(den > 0.f ? x / den : x);
+                    a.o[((size_t)cb * a.heads_q + head0 + r) * kD + tid] = __float2bfloat16_rn(quotient(x, R, M, den));
                 }
             }
         }
@@ -549,30 +606,34 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const Pa
     const int hkv = item / a.row_tiles, rt = item % a.row_tiles;
     const int rows = min(kHeadRows, a.group - rt * kHeadRows);
     for (int r = warp; r < rows; r += kCombineThreads / 32) {
-        float M = -INFINITY, den = 0.f;
+        float R = -INFINITY, M = -INFINITY, den = 0.f;
         bool bad = false;
         for (int c = c0 + lane; c <= c1; c += 32) {
-            const float2 ml = a.part_ml[((size_t)c * 2 + (c == c0 ? first : 0)) * a.rows + r];
-            M = fmaxf(M, ml.x);
-            bad |= ml.y < 0.f;
+            const float4 ml = a.part_ml[((size_t)c * 2 + (c == c0 ? first : 0)) * a.rows + r];
+            R = fmaxf(R, ml.x);
+            M = fmaxf(M, ml.y);
+            bad |= ml.w != 0.f;
         }
         if (__any_sync(0xffffffffu, bad)) continue;
 #pragma unroll
-        for (int d = 16; d >= 1; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+        for (int d = 16; d >= 1; d >>= 1) {
+            R = fmaxf(R, __shfl_xor_sync(0xffffffffu, R, d));
+            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+        }
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int c = c0; c <= c1; ++c) {
             const size_t at = ((size_t)c * 2 + (c == c0 ? first : 0)) * a.rows + r;
-            const float2 ml = a.part_ml[at];
-            const float f = ml.x == -INFINITY ? 0.f : ptx::ex2_approx(ml.x - M);
+            const float4 ml = a.part_ml[at];
+            const float f = weight(ml.x, R);
             const float4 v = reinterpret_cast<const float4 *>(a.part_o + at * kD)[lane];
             x.x = fmaf(f, v.x, x.x);
             x.y = fmaf(f, v.y, x.y);
             x.z = fmaf(f, v.z, x.z);
             x.w = fmaf(f, v.w, x.w);
-            den = fmaf(f, ml.y, den);
+            den = fmaf(weight(ml.y, M), ml.z, den);
         }
-        const float inv = den > 0.f ? 1.f / den : 1.f;
-        uint2 w = make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
+        const uint2 w = make_uint2(pack_bf16(quotient(x.x, R, M, den), quotient(x.y, R, M, den)),
+                                   pack_bf16(quotient(x.z, R, M, den), quotient(x.w, R, M, den)));
         reinterpret_cast<uint2 *>(a.o + ((size_t)b * a.heads_q + hkv * a.group + rt * kHeadRows + r) * kD)[lane] = w;
     }
 }
@@ -602,7 +663,7 @@ cudaError_t prepare(int *sms)
 
 bool heads_ok(int heads_q, int heads_kv) { return heads_q >= 1 && heads_kv >= 1 && heads_q % heads_kv == 0; }
 
-size_t paged_ws(int shares, int rows) { return (size_t)shares * 2 * rows * (kD * sizeof(float) + sizeof(float2)); }
+size_t paged_ws(int shares, int rows) { return (size_t)shares * 2 * rows * (kD * sizeof(float) + sizeof(float4)); }
 
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -667,7 +728,7 @@ extern "C" stree_status stree_paged_attention(const void *q, const void *k_pages
     a.lens = seq_len;
     a.o = static_cast<__nv_bfloat16 *>(o);
     a.part_o = static_cast<float *>(workspace);
-    a.part_ml = reinterpret_cast<float2 *>(a.part_o + (size_t)a.shares * 2 * a.rows * kD);
+    a.part_ml = reinterpret_cast<float4 *>(a.part_o + (size_t)a.shares * 2 * a.rows * kD);
     a.err = err_out;
     a.batch = batch;
     a.heads_q = heads_q;
