@@ -49,10 +49,14 @@ constexpr int kD = kCacheDim;
 constexpr int kBlk = 64;                       // positions per block
 constexpr int kComputeWarps = 4;               // 16 positions each
 constexpr int kThreads = (kComputeWarps + 1) * 32;
-constexpr int kHeadRows = 16;                  // query heads of a matrix instruction
+constexpr int kMaxHeads = 16;                  // query heads in a row of blocks
+constexpr int kJoinRow = kD + 4;               // floats of a row in shared memory (no bank conflicts)
 constexpr int kMaxStages = 8;
-constexpr int kSmemPerCta = 113 * 1024;        // two CTAs per SM
-constexpr int kCombineThreads = 128;
+
+// CTAs per SM: their warps hide one another's latencies, as many as registers and stages allow.
+__host__ __device__ constexpr int ctas_per_sm(bool e4m3, int nt) { return e4m3 && nt == 1 ? 3 : 2; }
+constexpr int smem_per_cta(int ctas) { return 226 * 1024 / ctas; }
+constexpr int kCombineWarps = 16, kCombineThreads = kCombineWarps * 32;
 
 struct PagedArgs {
     const __nv_bfloat16 *q;
@@ -127,6 +131,14 @@ __device__ __forceinline__ float quotient(float x, float ref, float m, float sum
     return sum > 0.f ? x * ptx::ex2_approx(ref - m) / sum : x;
 }
 
+// The transpose of an 8 x 8 tile of 16-bit elements held one row per four lanes.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x)
+{
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+
 struct Stage {                                 // offsets inside a stage of the ring
     uint32_t k, v, ks, vs, bytes;
 };
@@ -138,19 +150,21 @@ __host__ __device__ constexpr Stage stage_layout()
     return kE4m3 ? Stage{0, 8192, 16384, 16384 + 64, 16384 + 1024} : Stage{0, 16384, 0, 0, 32768};
 }
 
-template <bool kE4m3>
-__global__ void __launch_bounds__(kThreads, 2)
+// NT: tiles of eight query heads in a row of blocks.
+template <bool kE4m3, int NT>
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(kE4m3, NT))
 paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                        const PagedArgs a)
 {
     constexpr Stage L = stage_layout<kE4m3>();
+    constexpr int kHeads = 8 * NT;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ uint64_t bars[2 * kMaxStages];
     __shared__ int tmp[33], found[2];
     __shared__ volatile int aborted, bad[kMaxStages];
-    __shared__ float4 ml_s[kComputeWarps][kHeadRows];
+    __shared__ float4 ml_s[kComputeWarps][kHeads];
     uint8_t *smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
-    float *joined = reinterpret_cast<float *>(smem + a.stages * L.bytes);   // [4][rows][128]
+    float *joined = reinterpret_cast<float *>(smem + a.stages * L.bytes);   // [4][rows][132]
     auto full = [&](int s) { return ptx::smem_u32(&bars[s]); };
     auto empty = [&](int s) { return ptx::smem_u32(&bars[kMaxStages + s]); };
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -310,203 +324,204 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
     int piece = 0;                             // 0: the share's first row of blocks, 1: a later one
     while (left > 0 && run) {
         const int hkv = item / a.row_tiles, rt = item % a.row_tiles;
-        const int head0 = hkv * a.group + rt * kHeadRows;
-        const int rows = min(kHeadRows, a.group - rt * kHeadRows);
+        const int head0 = hkv * a.group + rt * kHeads;
+        const int rows = min(kHeads, a.group - rt * kHeads);
         const int cb = b, blk0 = blk, cnb = nb;
         const int n = min(max(__ldg(a.lens + cb), 0), a.max_pages * a.page_size);
         const bool whole = blk0 == 0 && left >= cnb;
-        // Q as the matrix instruction's A operand; rows past the group are zero.  With 8-bit
-        // pages the columns are permuted as the unpacked key bytes lie: k index 2 t, 2 t + 1
-        // of a step is column 4 t, 4 t + 1, and 2 t + 8, 2 t + 9 is 4 t + 2, 4 t + 3.
-        uint32_t qf[8][4];
-        float qs[2] = {a.scale_log2, a.scale_log2};
-        {
-            const __nv_bfloat16 *qp = a.q + ((size_t)cb * a.heads_q + head0) * kD;
+        // Q as the B operand: head r4 (+ 8 for the second tile), zero past the group.  With 8-bit
+        // pages the columns are permuted as the key bytes lie: k index 2 t, 2 t + 1 of a step is
+        // column 4 t, 4 t + 1, and 2 t + 8, 2 t + 9 is 4 t + 2, 4 t + 3.
+        uint32_t qf[NT][8][2];
+        float qs[NT][2];                       // log2-scale of the scores of heads 2 t4, 2 t4 + 1
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int head = t * 8 + r4;
+            const __nv_bfloat16 *qp = a.q + ((size_t)cb * a.heads_q + head0 + head) * kD;
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = r4 + (i & 1) * 8;
-                    const int col = kE4m3 ? kk * 16 + t4 * 4 + (i >> 1) * 2 : kk * 16 + t4 * 2 + (i >> 1) * 8;
-                    qf[kk][i] = r < rows ? __ldg(reinterpret_cast<const uint32_t *>(qp + (size_t)r * kD + col)) : 0u;
-                }
-            if (kE4m3) {
-#pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    uint32_t top = 0;
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk) top = max(top, max(finite_top2(qf[kk][i]), finite_top2(qf[kk][i + 2])));
-                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                    // The row's largest magnitude lies in [2^(e-127), 2^(e-126)).
-                    const uint32_t e = min(max(top >> 7, 2u), 252u);
-                    const float inv = power_of_two(253u - e);
-                    qs[i] *= power_of_two(e + 1u);
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-#pragma unroll
-                        for (int j = i; j < 4; j += 2) {
-                            const uint32_t w = qf[kk][j];
-                            const __half2 h = __floats2half2_rn(__uint_as_float(w << 16) * inv,
-                                                                __uint_as_float(w & 0xffff0000u) * inv);
-                            qf[kk][j] = *reinterpret_cast<const uint32_t *>(&h);
-                        }
+                    const int col = kE4m3 ? kk * 16 + t4 * 4 + i * 2 : kk * 16 + t4 * 2 + i * 8;
+                    qf[t][kk][i] = head < rows ? __ldg(reinterpret_cast<const uint32_t *>(qp + col)) : 0u;
                 }
+            float f = a.scale_log2;
+            if (kE4m3) {
+                uint32_t top = 0;
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk) top = max(top, max(finite_top2(qf[t][kk][0]), finite_top2(qf[t][kk][1])));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                // The row's largest magnitude lies in [2^(e-127), 2^(e-126)).
+                const uint32_t e = min(max(top >> 7, 2u), 252u);
+                const float inv = power_of_two(253u - e);
+                f *= power_of_two(e + 1u);
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t w = qf[t][kk][i];
+                        qf[t][kk][i] = pack_half(__uint_as_float(w << 16) * inv, __uint_as_float(w & 0xffff0000u) * inv);
+                    }
             }
+            qs[t][0] = __shfl_sync(0xffffffffu, f, t4 * 8);
+            qs[t][1] = __shfl_sync(0xffffffffu, f, t4 * 8 + 4);
         }
-        float acc[16][4];
+        float acc[NT][8][4];                   // 16 columns a step: rows r4, r4 + 8 of the tile, heads 2 t4, 2 t4 + 1
+        float m[NT][2], ref[NT][2], l[NT][2];
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
+        for (int t = 0; t < NT; ++t) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-        float m[2] = {-INFINITY, -INFINITY}, ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+            for (int c = 0; c < 8; ++c)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[t][c][j] = 0.f;
+            m[t][0] = m[t][1] = ref[t][0] = ref[t][1] = -INFINITY;
+            l[t][0] = l[t][1] = 0.f;
+        }
         int any_bad = 0;
+#pragma unroll 1
         while (true) {
             if (!(run = wait_warp(&aborted, full(s), phase, 10))) break;
             any_bad |= bad[s];
-            const uint32_t base = ptx::smem_u32(smem + s * L.bytes);
+            const uint32_t base = ptx::smem_u32(smem) + s * L.bytes;
             const int key0 = warp * 16, valid = n - (blk * kBlk + key0);   // positions of this warp that exist
             if (valid > 0) {
-                float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+                const bool tail = valid < 16;
+                // Scores: keys r4, r4 + 8 by heads 2 t4, 2 t4 + 1.
+                float sc[NT][4];
+#pragma unroll
+                for (int t = 0; t < NT; ++t) sc[t][0] = sc[t][1] = sc[t][2] = sc[t][3] = 0.f;
+                // Tiles of eight keys by 16 bytes: keys 0-7 and 8-15 of a chunk, then of the next.
+                const int krow = key0 + (lane & 15), ksw = krow & 7;
+                const uint32_t kaddr = base + L.k + krow * 128, vaddr = base + L.v;
                 if (kE4m3) {
-                    // Matrices: keys 0-7 and 8-15 of a 16-byte chunk, then of the next chunk.
-                    const int row = key0 + (lane & 15);
 #pragma unroll
                     for (int kk = 0; kk < 8; kk += 2) {
                         uint32_t r[4];
-                        ldsm4(base + L.k + row * 128 + (((kk + (lane >> 4)) ^ (row & 7)) << 4), r);
+                        ldsm4(kaddr + (((kk + (lane >> 4)) ^ ksw) << 4), r);
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
-                            mma16816<true>(sc[0], qf[kk + j], e4m3x2_to_f16x2(r[2 * j] & 0xffffu), e4m3x2_to_f16x2(r[2 * j] >> 16));
-                            mma16816<true>(sc[1], qf[kk + j], e4m3x2_to_f16x2(r[2 * j + 1] & 0xffffu), e4m3x2_to_f16x2(r[2 * j + 1] >> 16));
+                            uint32_t k[4];
+                            e4m3x4_to_f16(r[2 * j], k[0], k[2]);
+                            e4m3x4_to_f16(r[2 * j + 1], k[1], k[3]);
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) mma16816<true>(sc[t], k, qf[t][kk + j][0], qf[t][kk + j][1]);
                         }
                     }
                 } else {
-                    const int row = key0 + (lane & 7) + ((lane >> 4) << 3);
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk) {
                         uint32_t r[4];
-                        const int chunk = kk * 2 + ((lane >> 3) & 1);
-                        ldsm4(base + L.k + (chunk >> 3) * 8192 + row * 128 + (((chunk & 7) ^ (row & 7)) << 4), r);
-                        mma16816<false>(sc[0], qf[kk], r[0], r[1]);
-                        mma16816<false>(sc[1], qf[kk], r[2], r[3]);
+                        const int chunk = kk * 2 + (lane >> 4);
+                        ldsm4(kaddr + (chunk >> 3) * 8192 + (((chunk & 7) ^ ksw) << 4), r);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) mma16816<false>(sc[t], r, qf[t][kk][0], qf[t][kk][1]);
                     }
                 }
-                // This thread's scores: rows r4 and r4 + 8, positions key0 + 8 j + 2 t4 + {0, 1}.
-                const bool tail = valid < 16;
-                float ve[4] = {0.f, 0.f, 0.f, 0.f};   // log2 of the values' scales
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    float f[2][2] = {{qs[0], qs[0]}, {qs[1], qs[1]}};
-                    if (kE4m3) {
-                        const uint8_t *sb = smem + s * L.bytes + key0 + 8 * j + 2 * t4;
-                        const uint32_t kb = *reinterpret_cast<const uint16_t *>(sb + L.ks), vb = *reinterpret_cast<const uint16_t *>(sb + L.vs);
-                        const float k0 = power_of_two(kb & 0xffu), k1 = power_of_two(kb >> 8);
-                        ve[2 * j] = __uint_as_float(0x4b000000u | (vb & 0xffu)) - 8388735.f;   // 2^23 + byte, less 2^23 + 127
-                        ve[2 * j + 1] = __uint_as_float(0x4b000000u | (vb >> 8)) - 8388735.f;
-                        f[0][0] *= k0;
-                        f[0][1] *= k1;
-                        f[1][0] *= k0;
-                        f[1][1] *= k1;
-                    }
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) sc[j][2 * i + e] *= f[i][e];
-                }
-                if (tail)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (8 * j + 2 * t4 + (e & 1) >= valid) sc[j][e] = -INFINITY;
-                // Running maxima of the scores and, for the output, of the scores with the values' scales.
-                float mn[2], rn[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    mn[i] = fmaxf(fmaxf(sc[0][2 * i], sc[0][2 * i + 1]), fmaxf(sc[1][2 * i], sc[1][2 * i + 1]));
-                    mn[i] = fmaxf(mn[i], __shfl_xor_sync(0xffffffffu, mn[i], 1));
-                    mn[i] = fmaxf(m[i], fmaxf(mn[i], __shfl_xor_sync(0xffffffffu, mn[i], 2)));
-                    rn[i] = mn[i];
-                    if (kE4m3) {
-                        rn[i] = fmaxf(fmaxf(sc[0][2 * i] + ve[0], sc[0][2 * i + 1] + ve[1]), fmaxf(sc[1][2 * i] + ve[2], sc[1][2 * i + 1] + ve[3]));
-                        rn[i] = fmaxf(rn[i], __shfl_xor_sync(0xffffffffu, rn[i], 1));
-                        rn[i] = fmaxf(ref[i], fmaxf(rn[i], __shfl_xor_sync(0xffffffffu, rn[i], 2)));
-                    }
-                }
-                if (__any_sync(0xffffffffu, mn[0] > m[0] || mn[1] > m[1] || rn[0] > ref[0] || rn[1] > ref[1])) {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float f = rn[i] == ref[i] ? 1.f : ptx::ex2_approx(ref[i] - rn[i]);
-                        l[i] *= mn[i] == m[i] ? 1.f : ptx::ex2_approx(m[i] - mn[i]);
-                        m[i] = mn[i];
-                        ref[i] = rn[i];
-#pragma unroll
-                        for (int c = 0; c < 16; ++c) {
-                            acc[c][2 * i] *= f;
-                            acc[c][2 * i + 1] *= f;
-                        }
-                    }
-                }
-                uint32_t pf[4];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float mi = m[i] == -INFINITY ? 0.f : m[i], ri = ref[i] == -INFINITY ? 0.f : ref[i];
+                float kf[2] = {1.f, 1.f}, ve[2] = {0.f, 0.f};   // a key's scale, log2 of a value's
+                if (kE4m3) {
+                    const uint8_t *sb = smem + s * L.bytes + key0 + r4;
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        const float p0 = ptx::ex2_approx(sc[j][2 * i] - mi), p1 = ptx::ex2_approx(sc[j][2 * i + 1] - mi);
-                        l[i] += p0 + p1;
-                        pf[2 * j + i] = kE4m3 ? pack_half(ptx::ex2_approx(sc[j][2 * i] + (ve[2 * j] - ri)),
-                                                          ptx::ex2_approx(sc[j][2 * i + 1] + (ve[2 * j + 1] - ri)))
-                                              : pack_bf16(p0, p1);
+                        kf[j] = power_of_two(sb[L.ks + 8 * j]);
+                        ve[j] = __uint_as_float(0x4b000000u | sb[L.vs + 8 * j]) - 8388735.f;   // 2^23 + byte, less 2^23 + 127
+                    }
+                }
+                uint32_t pf[NT][2];
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        sc[t][e] *= kE4m3 ? qs[t][e & 1] * kf[e >> 1] : qs[t][e & 1];
+                        if (tail && r4 + 8 * (e >> 1) >= valid) sc[t][e] = -INFINITY;
+                    }
+                    // Running maxima of the scores and, for the output, of the scores with the values' scales.
+                    float mn[2], rn[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        mn[i] = fmaxf(sc[t][i], sc[t][2 + i]);
+                        rn[i] = fmaxf(sc[t][i] + ve[0], sc[t][2 + i] + ve[1]);
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) {
+                            mn[i] = fmaxf(mn[i], __shfl_xor_sync(0xffffffffu, mn[i], d));
+                            if (kE4m3) rn[i] = fmaxf(rn[i], __shfl_xor_sync(0xffffffffu, rn[i], d));
+                        }
+                        mn[i] = fmaxf(m[t][i], mn[i]);
+                        rn[i] = kE4m3 ? fmaxf(ref[t][i], rn[i]) : mn[i];
+                    }
+                    if (__any_sync(0xffffffffu, mn[0] > m[t][0] || mn[1] > m[t][1] || rn[0] > ref[t][0] || rn[1] > ref[t][1])) {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float f = rn[i] == ref[t][i] ? 1.f : ptx::ex2_approx(ref[t][i] - rn[i]);
+                            l[t][i] *= mn[i] == m[t][i] ? 1.f : ptx::ex2_approx(m[t][i] - mn[i]);
+                            m[t][i] = mn[i];
+                            ref[t][i] = rn[i];
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) {
+                                acc[t][c][i] *= f;
+                                acc[t][c][2 + i] *= f;
+                            }
+                        }
+                    }
+                    // Probabilities; turned from (key, head) to the B operand's (head, key) by a transposing move.
+                    const float m0 = m[t][0] == -INFINITY ? 0.f : m[t][0], m1 = m[t][1] == -INFINITY ? 0.f : m[t][1];
+                    const float r0 = ref[t][0] == -INFINITY ? 0.f : ref[t][0], r1 = ref[t][1] == -INFINITY ? 0.f : ref[t][1];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float p0 = ptx::ex2_approx(sc[t][2 * j] - m0), p1 = ptx::ex2_approx(sc[t][2 * j + 1] - m1);
+                        l[t][0] += p0;
+                        l[t][1] += p1;
+                        pf[t][j] = transpose8(kE4m3 ? pack_half(ptx::ex2_approx(sc[t][2 * j] + (ve[j] - r0)),
+                                                                ptx::ex2_approx(sc[t][2 * j + 1] + (ve[j] - r1)))
+                                                    : pack_bf16(p0, p1));
                     }
                 }
                 // Positions past the end hold anything: their value rows count as zero.
                 const uint32_t keep0 = (2 * t4 < valid ? 0xffffu : 0u) | (2 * t4 + 1 < valid ? 0xffff0000u : 0u);
                 const uint32_t keep1 = (2 * t4 + 8 < valid ? 0xffffu : 0u) | (2 * t4 + 9 < valid ? 0xffff0000u : 0u);
-                const int row = key0 + (lane & 15);
                 if (kE4m3) {
-                    // Matrices: keys 0-7 and 8-15 of a 16-byte chunk, then of the next.  A thread gets
-                    // columns 2 r4, 2 r4 + 1 of keys 2 t4, 2 t4 + 1: the even columns make one
-                    // instruction's operand, the odd ones another's.
+                    // A thread gets columns 2 r4, 2 r4 + 1 of keys 2 t4, 2 t4 + 1: the even columns are
+                    // the operand's rows 0-7, the odd ones its rows 8-15.
 #pragma unroll
                     for (int c = 0; c < 8; c += 2) {
                         uint32_t r[4];
-                        ldsm4_t(base + L.v + row * 128 + (((c + (lane >> 4)) ^ (row & 7)) << 4), r);
+                        ldsm4_t(vaddr + krow * 128 + (((c + (lane >> 4)) ^ ksw) << 4), r);
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
-                            const uint32_t x = __byte_perm(r[2 * j], 0, 0x3120), y = __byte_perm(r[2 * j + 1], 0, 0x3120);
-                            uint32_t v[4] = {e4m3x2_to_f16x2(x & 0xffffu), e4m3x2_to_f16x2(y & 0xffffu), e4m3x2_to_f16x2(x >> 16),
-                                             e4m3x2_to_f16x2(y >> 16)};
+                            uint32_t v[4];
+                            e4m3x4_to_f16(__byte_perm(r[2 * j], 0, 0x3120), v[0], v[1]);
+                            e4m3x4_to_f16(__byte_perm(r[2 * j + 1], 0, 0x3120), v[2], v[3]);
                             if (tail) {
                                 v[0] &= keep0;
-                                v[1] &= keep1;
-                                v[2] &= keep0;
+                                v[1] &= keep0;
+                                v[2] &= keep1;
                                 v[3] &= keep1;
                             }
-                            mma16816<true>(acc[2 * (c + j)], pf, v[0], v[1]);
-                            mma16816<true>(acc[2 * (c + j) + 1], pf, v[2], v[3]);
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) mma16816<true>(acc[t][c + j], v, pf[t][0], pf[t][1]);
                         }
                     }
                 } else {
+                    // Tiles: keys 0-7 of two chunks of eight columns, then keys 8-15.
+                    const int vrow = key0 + (lane & 7) + ((lane >> 4) << 3);
 #pragma unroll
                     for (int c = 0; c < 8; ++c) {
-                        uint32_t r[4];
-                        const int chunk = 2 * c + (lane >> 4);
-                        ldsm4_t(base + L.v + (chunk >> 3) * 8192 + row * 128 + (((chunk & 7) ^ (row & 7)) << 4), r);
+                        uint32_t v[4];
+                        const int chunk = 2 * c + ((lane >> 3) & 1);
+                        ldsm4_t(vaddr + (chunk >> 3) * 8192 + vrow * 128 + (((chunk & 7) ^ (vrow & 7)) << 4), v);
                         if (tail) {
-                            r[0] &= keep0;
-                            r[1] &= keep1;
-                            r[2] &= keep0;
-                            r[3] &= keep1;
+                            v[0] &= keep0;
+                            v[1] &= keep0;
+                            v[2] &= keep1;
+                            v[3] &= keep1;
                         }
-                        mma16816<false>(acc[2 * c], pf, r[0], r[1]);
-                        mma16816<false>(acc[2 * c + 1], pf, r[2], r[3]);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) mma16816<false>(acc[t][c], v, pf[t][0], pf[t][1]);
                     }
                 }
             }
             __syncwarp();
-            if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(empty(s)) : "memory");
+            if (lane == 0) ptx::mbar_arrive(empty(s));
             if (++s == a.stages) {
                 s = 0;
                 ++phase;
@@ -518,25 +533,25 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
         }
         // Join the four warps: each leaves its rows, then a thread takes one column.
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-            const int r = r4 + 8 * i;
-            if (r >= rows) continue;
-            if (t4 == 0) ml_s[warp][r] = make_float4(ref[i], m[i], l[i], 0.f);
-            float *dst = joined + ((size_t)warp * a.rows + r) * kD;
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                if (kE4m3) {
-                    // Columns 16 c + 4 t4 + {0, 2} and {1, 3}.
-                    *reinterpret_cast<float4 *>(dst + 16 * c + 4 * t4) =
-                        make_float4(acc[2 * c][2 * i], acc[2 * c + 1][2 * i], acc[2 * c][2 * i + 1], acc[2 * c + 1][2 * i + 1]);
-                } else {
-                    *reinterpret_cast<float2 *>(dst + 16 * c + 2 * t4) = make_float2(acc[2 * c][2 * i], acc[2 * c][2 * i + 1]);
-                    *reinterpret_cast<float2 *>(dst + 16 * c + 8 + 2 * t4) = make_float2(acc[2 * c + 1][2 * i], acc[2 * c + 1][2 * i + 1]);
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) l[t][i] += __shfl_xor_sync(0xffffffffu, l[t][i], d);
+                const int r = t * 8 + 2 * t4 + i;
+                if (r >= rows) continue;
+                if (r4 == 0) ml_s[warp][r] = make_float4(ref[t][i], m[t][i], l[t][i], 0.f);
+                float *dst = joined + ((size_t)warp * a.rows + r) * kJoinRow;
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    if (kE4m3) {
+                        *reinterpret_cast<float2 *>(dst + 16 * c + 2 * r4) = make_float2(acc[t][c][i], acc[t][c][2 + i]);
+                    } else {
+                        dst[16 * c + r4] = acc[t][c][i];
+                        dst[16 * c + 8 + r4] = acc[t][c][2 + i];
+                    }
                 }
             }
-        }
         asm volatile("bar.sync 1, %0;" ::"n"(kComputeWarps * 32) : "memory");
         if (!aborted) {
             const size_t slot = (size_t)blockIdx.x * 2 + piece;
@@ -550,7 +565,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
 #pragma unroll
                 for (int w = 0; w < kComputeWarps; ++w) {
                     const float4 ml = ml_s[w][r];
-                    x = fmaf(weight(ml.x, R), joined[((size_t)w * a.rows + r) * kD + tid], x);
+                    x = fmaf(weight(ml.x, R), joined[((size_t)w * a.rows + r) * kJoinRow + tid], x);
                     den = fmaf(weight(ml.y, M), ml.z, den);
                 }
                 if (!whole) {
@@ -577,11 +592,15 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
 }
 
 // Joins the pieces of every row of blocks that more than one share holds.  One block per
-// (sequence, key/value head, row tile); a warp per query head, four columns per lane.
+// (sequence, key/value head, row tile); its warps share out the query heads and, with few of
+// those, the pieces of a head (one long sequence has as many pieces as an eighth of the
+// shares: read one after the other they took 17 us of 100, four at a time in four warps 4).
+// A lane has four columns.
 __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const PagedArgs a)
 {
     __shared__ int tmp[33];
     __shared__ int before_s;
+    __shared__ float4 sums[kCombineWarps][32];
     pdl_start();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per_seq = a.heads_kv * a.row_tiles;
@@ -600,42 +619,63 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const Pa
     const long long begin = (long long)before_s * per_seq + (long long)item * nb, end = begin + nb;
     // The share that holds block x: the last c with share_begin(c) <= x.
     const int shares = (int)min((long long)a.shares, total);
-    const int c0 = (int)(((begin + 1) * shares - 1) / total), c1 = (int)((end * shares - 1) / total);
-    if (c0 == c1) return;
+    const int c0 = (int)(((begin + 1) * shares - 1) / total), pieces = (int)((end * shares - 1) / total) - c0 + 1;
+    if (pieces == 1) return;
     const int first = share_begin(total, c0, shares) == begin ? 0 : 1;
     const int hkv = item / a.row_tiles, rt = item % a.row_tiles;
-    const int rows = min(kHeadRows, a.group - rt * kHeadRows);
-    for (int r = warp; r < rows; r += kCombineThreads / 32) {
-        float R = -INFINITY, M = -INFINITY, den = 0.f;
-        bool bad = false;
-        for (int c = c0 + lane; c <= c1; c += 32) {
-            const float4 ml = a.part_ml[((size_t)c * 2 + (c == c0 ? first : 0)) * a.rows + r];
+    const int heads = a.group <= 8 ? 8 : kMaxHeads;
+    const int rows = min(heads, a.group - rt * heads);
+    int slices = kCombineWarps / rows;         // warps of a head, at most one per piece
+    slices = min(max(slices, 1), pieces);
+    const int r = warp / slices, slice = warp % slices;
+    const bool mine = r < rows;
+    auto at = [&](int k) { return ((size_t)(c0 + k) * 2 + (k == 0 ? first : 0)) * a.rows + r; };
+    float R = -INFINITY, M = -INFINITY, den = 0.f;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    bool bad = false;
+    if (mine) {
+        for (int k = lane; k < pieces; k += 32) {
+            const float4 ml = a.part_ml[at(k)];
             R = fmaxf(R, ml.x);
             M = fmaxf(M, ml.y);
             bad |= ml.w != 0.f;
         }
-        if (__any_sync(0xffffffffu, bad)) continue;
+        bad = __any_sync(0xffffffffu, bad);
 #pragma unroll
         for (int d = 16; d >= 1; d >>= 1) {
             R = fmaxf(R, __shfl_xor_sync(0xffffffffu, R, d));
             M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
         }
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int c = c0; c <= c1; ++c) {
-            const size_t at = ((size_t)c * 2 + (c == c0 ? first : 0)) * a.rows + r;
-            const float4 ml = a.part_ml[at];
+#pragma unroll 4
+        for (int k = slice; k < pieces; k += slices) {
+            const float4 ml = a.part_ml[at(k)];
+            const float4 v = reinterpret_cast<const float4 *>(a.part_o + at(k) * kD)[lane];
             const float f = weight(ml.x, R);
-            const float4 v = reinterpret_cast<const float4 *>(a.part_o + at * kD)[lane];
             x.x = fmaf(f, v.x, x.x);
             x.y = fmaf(f, v.y, x.y);
             x.z = fmaf(f, v.z, x.z);
             x.w = fmaf(f, v.w, x.w);
-            den = fmaf(weight(ml.y, M), ml.z, den);
         }
-        const uint2 w = make_uint2(pack_bf16(quotient(x.x, R, M, den), quotient(x.y, R, M, den)),
-                                   pack_bf16(quotient(x.z, R, M, den), quotient(x.w, R, M, den)));
-        reinterpret_cast<uint2 *>(a.o + ((size_t)b * a.heads_q + hkv * a.group + rt * kHeadRows + r) * kD)[lane] = w;
+        sums[warp][lane] = x;
     }
+    __syncthreads();
+    if (!mine || bad || slice != 0) return;
+    for (int k = lane; k < pieces; k += 32) {
+        const float4 ml = a.part_ml[at(k)];
+        den = fmaf(weight(ml.y, M), ml.z, den);
+    }
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) den += __shfl_xor_sync(0xffffffffu, den, d);
+    for (int w = 1; w < slices; ++w) {
+        const float4 v = sums[warp + w][lane];
+        x.x += v.x;
+        x.y += v.y;
+        x.z += v.z;
+        x.w += v.w;
+    }
+    const uint2 w = make_uint2(pack_bf16(quotient(x.x, R, M, den), quotient(x.y, R, M, den)),
+                               pack_bf16(quotient(x.z, R, M, den), quotient(x.w, R, M, den)));
+    reinterpret_cast<uint2 *>(a.o + ((size_t)b * a.heads_q + hkv * a.group + rt * heads + r) * kD)[lane] = w;
 }
 
 constexpr int kMaxDevices = 64;
@@ -650,8 +690,13 @@ cudaError_t prepare(int *sms)
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
     std::lock_guard<std::mutex> lock(g_mutex);
     if (!g_sms[dev]) {
-        if ((e = cudaFuncSetAttribute(paged_attention_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerCta)) != cudaSuccess ||
-            (e = cudaFuncSetAttribute(paged_attention_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerCta)) != cudaSuccess)
+        const auto set = [](auto *f, bool e4m3, int nt) {
+            return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_per_cta(ctas_per_sm(e4m3, nt)));
+        };
+        if ((e = set(paged_attention_kernel<false, 1>, false, 1)) != cudaSuccess ||
+            (e = set(paged_attention_kernel<false, 2>, false, 2)) != cudaSuccess ||
+            (e = set(paged_attention_kernel<true, 1>, true, 1)) != cudaSuccess ||
+            (e = set(paged_attention_kernel<true, 2>, true, 2)) != cudaSuccess)
             return e;
         int n = 0;
         if ((e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
@@ -679,7 +724,7 @@ extern "C" stree_status stree_paged_attention_workspace_size(int heads_q, int he
     int sms = 0;
     if (prepare(&sms) != cudaSuccess) return STREE_ERR_CUDA;
     const int group = heads_q / heads_kv;
-    *bytes = paged_ws(2 * sms, group < kHeadRows ? group : kHeadRows);
+    *bytes = paged_ws(3 * sms, group < kMaxHeads ? group : kMaxHeads);
     return STREE_OK;
 }
 
@@ -702,8 +747,9 @@ extern "C" stree_status stree_paged_attention(const void *q, const void *k_pages
         return STREE_ERR_MISALIGNED;
     PagedArgs a{};
     a.group = heads_q / heads_kv;
-    a.rows = a.group < kHeadRows ? a.group : kHeadRows;
-    a.row_tiles = (a.group + kHeadRows - 1) / kHeadRows;
+    const int nt = a.group <= 8 ? 1 : 2;
+    a.rows = a.group < 8 * nt ? a.group : 8 * nt;
+    a.row_tiles = (a.group + 8 * nt - 1) / (8 * nt);
     const long long blocks = ((long long)max_pages * page_size + kBlk - 1) / kBlk;
     if (blocks * batch > 0x7fffffffLL || (long long)batch * heads_kv * a.row_tiles > 0x7fffffffLL)
         return STREE_ERR_UNSUPPORTED;
@@ -711,10 +757,11 @@ extern "C" stree_status stree_paged_attention(const void *q, const void *k_pages
     if (prepare(&sms) != cudaSuccess) return STREE_ERR_CUDA;
     // As many shares as the SMs hold CTAs, and no more than there can be blocks.
     const long long most = blocks * batch * heads_kv * a.row_tiles;
-    a.shares = (int)(most < 2LL * sms ? most : 2LL * sms);
+    const bool e4m3 = cache_dtype == STREE_E4M3;
+    const int ctas = ctas_per_sm(e4m3, nt);
+    a.shares = (int)(most < (long long)ctas * sms ? most : (long long)ctas * sms);
     const size_t need = paged_ws(a.shares, a.rows);
     if (workspace_bytes < need) return STREE_ERR_INVALID_ARG;
-    const bool e4m3 = cache_dtype == STREE_E4M3;
     a.box_rows = 8;
     while (a.box_rows < kBlk && page_size % (2 * a.box_rows) == 0) a.box_rows *= 2;
     const long long rows = (long long)n_pages * heads_kv * page_size;
@@ -738,13 +785,14 @@ extern "C" stree_status stree_paged_attention(const void *q, const void *k_pages
     a.max_pages = max_pages;
     a.scale_log2 = scale * 1.4426950408889634f;
     const int stage = e4m3 ? stage_layout<true>().bytes : stage_layout<false>().bytes;
-    const int join = kComputeWarps * a.rows * kD * (int)sizeof(float), slack = 1024, fixed = 2048;
-    a.stages = (kSmemPerCta - join - slack - fixed) / stage;
+    const int join = kComputeWarps * a.rows * kJoinRow * (int)sizeof(float), slack = 1024, fixed = 3072;
+    a.stages = (smem_per_cta(ctas) - join - slack - fixed) / stage;
     if (a.stages > kMaxStages) a.stages = kMaxStages;
     const size_t smem = (size_t)a.stages * stage + join + slack;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = launch_pdl(e4m3 ? paged_attention_kernel<true> : paged_attention_kernel<false>,
-                                     dim3((unsigned)a.shares + 1), kThreads, smem, s, m_k, m_v, a);
+    const auto kernel = e4m3 ? (nt == 1 ? paged_attention_kernel<true, 1> : paged_attention_kernel<true, 2>)
+                             : (nt == 1 ? paged_attention_kernel<false, 1> : paged_attention_kernel<false, 2>);
+    const cudaError_t e = launch_pdl(kernel, dim3((unsigned)a.shares + 1), kThreads, smem, s, m_k, m_v, a);
     if (e != cudaSuccess) return STREE_ERR_CUDA;
     return launch_pdl(paged_combine_kernel, dim3((unsigned)(batch * heads_kv * a.row_tiles)), kCombineThreads, 0, s, a) ==
                    cudaSuccess

@@ -208,6 +208,17 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w)
     return r;
 }
 
+// Four e4m3 -> two pairs of fp16, exactly.
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi)
+{
+    asm("{\n\t.reg .b16 l, h;\n\t"
+        "mov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
+
 // Two e4m3 times a power of two -> two bf16, exactly (a scale within [9, 246]).
 __device__ __forceinline__ uint32_t dequantise2(uint32_t w, float scale)
 {
