@@ -2,19 +2,20 @@
 // path into pages (bf16, or quantised to e4m3 as it is written), and reading pages
 // back into the contiguous cache of the tree-masked attention, sm_100a.
 //
-// Every row is 128 values of one (token, key/value head), so a row is the unit of
-// the copy and of the quantisation: 16 lanes hold it, 8 values (16 bytes) each, take
-// the largest magnitude by four shuffles and store 8 bytes each.  Nothing is reused,
-// so the kernels are bound by HBM: the keys and the values of a row are moved by the
-// same lanes (two independent 16-byte loads in flight for each thread, and as many
-// threads as the SM holds).
+// Every row is 128 values of one (token, key/value head): 16 lanes hold it, 8 values (16
+// bytes) each, take the largest magnitude by four shuffles and store 8 bytes each.  Nothing is
+// reused, so the kernels are bound by HBM, and a thread's chain of look-ups (sequence, page)
+// has to be paid by enough data: 16 lanes take four heads of a token, keys and values, eight
+// independent 16-byte loads in flight for each thread (8192 tokens of 8 heads written to e4m3
+// pages and read back, 101 MB: 24.9 us; with a head at a time 30.1).
 #include "seq_pages.cuh"
 
 namespace stree {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRowsPerBlock = kThreads / 16;
+constexpr int kHeadsPerUnit = 4;               // heads of a token that 16 lanes take
+constexpr int kUnitsPerBlock = kThreads / 16;
 
 struct CacheArgs {
     const uint16_t *k, *v;                     // packed rows (write, commit)
@@ -59,14 +60,34 @@ __device__ __forceinline__ void put(const uint4 &x, uint8_t *pages, uint8_t *sca
     if (l16 == 0) scales[slot] = (uint8_t)s;
 }
 
+// 8 values of a page slot as they lie there (the scale beside them), and as bf16.
+struct Held {
+    uint4 x;
+    uint32_t scale;
+};
+
 template <bool kE4m3>
-__device__ __forceinline__ uint4 take(const uint8_t *pages, const uint8_t *scales, size_t slot, int l16)
+__device__ __forceinline__ Held take(const uint8_t *pages, const uint8_t *scales, size_t slot, int l16)
 {
-    if (!kE4m3) return __ldg(reinterpret_cast<const uint4 *>(pages + slot * (kCacheDim * 2) + l16 * 16));
-    const uint2 r = __ldg(reinterpret_cast<const uint2 *>(pages + slot * kCacheDim + l16 * 8));
-    const float s = power_of_two(__ldg(scales + slot));
-    return make_uint4(dequantise2(r.x & 0xffffu, s), dequantise2(r.x >> 16, s), dequantise2(r.y & 0xffffu, s),
-                      dequantise2(r.y >> 16, s));
+    Held h{};
+    if (kE4m3) {
+        const uint2 r = __ldcs(reinterpret_cast<const uint2 *>(pages + slot * kCacheDim + l16 * 8));
+        h.x.x = r.x;
+        h.x.y = r.y;
+        h.scale = __ldg(scales + slot);
+    } else {
+        h.x = __ldcs(reinterpret_cast<const uint4 *>(pages + slot * (kCacheDim * 2) + l16 * 16));
+    }
+    return h;
+}
+
+template <bool kE4m3>
+__device__ __forceinline__ uint4 values(const Held &h)
+{
+    if (!kE4m3) return h.x;
+    const float s = power_of_two(h.scale);
+    return make_uint4(dequantise2(h.x.x & 0xffffu, s), dequantise2(h.x.x >> 16, s), dequantise2(h.x.y & 0xffffu, s),
+                      dequantise2(h.x.y >> 16, s));
 }
 
 template <Mode kMode, bool kE4m3>
@@ -98,61 +119,82 @@ __global__ void __launch_bounds__(kThreads) cache_kernel(const CacheArgs a)
     }
     const int l16 = threadIdx.x & 15;
     const uint32_t mask = threadIdx.x & 16 ? 0xffff0000u : 0x0000ffffu;
-    const long long row = (long long)blockIdx.x * kRowsPerBlock + (threadIdx.x >> 4);
-    const int h = (int)(row % a.heads);
-    const long long tok = row / a.heads;
+    const uint32_t unit = blockIdx.x * kUnitsPerBlock + (threadIdx.x >> 4);   // below 2^31 (checked on the host)
+    const uint32_t per_tok = (a.heads + kHeadsPerUnit - 1) / kHeadsPerUnit;
+    const int tok = (int)(unit / per_tok), h0 = (int)(unit % per_tok) * kHeadsPerUnit;
     int b, pos;
-    size_t src;                                // row of k / v, or of k_ctx / v_ctx
+    size_t src;                                // token row of k / v, or of k_ctx / v_ctx
     if (kMode == kWrite) {
         if (tok >= a.total) return;
-        b = seq_of_row(a.cu, a.batch, (int)tok);
+        b = seq_of_row(a.cu, a.batch, tok);
         const int2 r = seq_range(a.cu, b, a.total);
         if (tok < r.x || tok >= r.y) return;   // behind the last sequence
-        pos = (int)tok - r.x;
         const int at = __ldg(a.start + b);
         if (at < 0 || (long long)at + (r.y - r.x) > (long long)a.max_pages * a.page_size) return;
-        pos += at;
-        src = (size_t)tok * a.heads + h;
+        pos = tok - r.x + at;
+        src = (size_t)tok;
     } else if (kMode == kCommit) {
-        b = (int)(tok / a.maxlen);
+        b = tok / a.maxlen;
         if (b >= a.batch) return;
-        const int j = (int)(tok % a.maxlen), n = min(max(__ldg(a.path_len + b), 0), a.maxlen);
+        const int j = tok % a.maxlen, n = min(max(__ldg(a.path_len + b), 0), a.maxlen);
         if (j >= n) return;
         const int node = __ldg(a.path + tok), at = __ldg(a.start + b);
         if (node < 0 || node >= a.n_nodes || at < 0 || (long long)at + n > (long long)a.max_pages * a.page_size) return;
         pos = at + j;
-        src = ((size_t)b * a.n_nodes + node) * a.heads + h;
+        src = (size_t)b * a.n_nodes + node;
     } else {
-        b = (int)(tok / a.ctx_cap);
+        b = tok / a.ctx_cap;
         if (b >= a.batch) return;
-        pos = (int)(tok % a.ctx_cap);
+        pos = tok % a.ctx_cap;
         if (pos >= min((long long)__ldg(a.lens + b), (long long)a.max_pages * a.page_size)) return;
-        src = (size_t)tok * a.heads + h;
+        src = (size_t)tok;
     }
     const int page = __ldg(a.table + (size_t)b * a.max_pages + pos / a.page_size);
     if (page < 0 || page >= a.n_pages) return;
-    const size_t slot = ((size_t)page * a.heads + h) * a.page_size + pos % a.page_size;
+    const size_t slot0 = ((size_t)page * a.heads + h0) * a.page_size + pos % a.page_size;
+    const size_t row0 = (src * a.heads + h0) * kCacheDim + l16 * 8;
+    const int n = min(kHeadsPerUnit, a.heads - h0);
     if (kMode == kRead) {
-        const uint4 k = take<kE4m3>(a.k_pages, a.k_scales, slot, l16), v = take<kE4m3>(a.v_pages, a.v_scales, slot, l16);
-        *reinterpret_cast<uint4 *>(a.k_ctx + src * kCacheDim + l16 * 8) = k;
-        *reinterpret_cast<uint4 *>(a.v_ctx + src * kCacheDim + l16 * 8) = v;
+        Held k[kHeadsPerUnit], v[kHeadsPerUnit];
+#pragma unroll
+        for (int h = 0; h < kHeadsPerUnit; ++h)
+            if (h < n) {
+                k[h] = take<kE4m3>(a.k_pages, a.k_scales, slot0 + (size_t)h * a.page_size, l16);
+                v[h] = take<kE4m3>(a.v_pages, a.v_scales, slot0 + (size_t)h * a.page_size, l16);
+            }
+#pragma unroll
+        for (int h = 0; h < kHeadsPerUnit; ++h)
+            if (h < n) {
+                *reinterpret_cast<uint4 *>(a.k_ctx + row0 + h * kCacheDim) = values<kE4m3>(k[h]);
+                *reinterpret_cast<uint4 *>(a.v_ctx + row0 + h * kCacheDim) = values<kE4m3>(v[h]);
+            }
     } else {
-        const uint4 k = __ldg(reinterpret_cast<const uint4 *>(a.k + src * kCacheDim + l16 * 8));
-        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(a.v + src * kCacheDim + l16 * 8));
-        put<kE4m3>(k, a.k_pages, a.k_scales, slot, l16, mask);
-        put<kE4m3>(v, a.v_pages, a.v_scales, slot, l16, mask);
+        uint4 k[kHeadsPerUnit], v[kHeadsPerUnit];
+#pragma unroll
+        for (int h = 0; h < kHeadsPerUnit; ++h)
+            if (h < n) {
+                k[h] = __ldcs(reinterpret_cast<const uint4 *>(a.k + row0 + h * kCacheDim));
+                v[h] = __ldcs(reinterpret_cast<const uint4 *>(a.v + row0 + h * kCacheDim));
+            }
+#pragma unroll
+        for (int h = 0; h < kHeadsPerUnit; ++h)
+            if (h < n) {                       // the same for a unit's 16 lanes
+                put<kE4m3>(k[h], a.k_pages, a.k_scales, slot0 + (size_t)h * a.page_size, l16, mask);
+                put<kE4m3>(v[h], a.v_pages, a.v_scales, slot0 + (size_t)h * a.page_size, l16, mask);
+            }
     }
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
 
-// Rows to cover -> blocks, one more for the error word.
+// Tokens to cover -> blocks, one more for the error word.
 template <Mode kMode>
 stree_status launch_cache(const CacheArgs &a, stree_dtype cache, long long tokens, void *stream)
 {
-    const long long blocks = (tokens * a.heads + kRowsPerBlock - 1) / kRowsPerBlock + 1;
-    if (blocks > 0x7fffffffLL) return STREE_ERR_UNSUPPORTED;
+    const long long units = tokens * ((a.heads + kHeadsPerUnit - 1) / kHeadsPerUnit);
+    if (units > 0x7fffff00LL) return STREE_ERR_UNSUPPORTED;
+    const long long blocks = (units + kUnitsPerBlock - 1) / kUnitsPerBlock + 1;
     const cudaError_t e = launch_pdl(cache == STREE_E4M3 ? cache_kernel<kMode, true> : cache_kernel<kMode, false>,
                                      dim3((unsigned)blocks), kThreads, 0, static_cast<cudaStream_t>(stream), a);
     return e == cudaSuccess ? STREE_OK : STREE_ERR_CUDA;
@@ -169,7 +211,7 @@ stree_status check_cache(const void *k_pages, const void *v_pages, const void *k
         page_size > 4096 || page_size % 8 != 0 || (cache != STREE_BF16 && cache != STREE_E4M3))
         return STREE_ERR_UNSUPPORTED;
     // Positions and page rows are 32-bit numbers inside the kernels (byte offsets are not).
-    if ((long long)n_pages * page_size * heads_kv > 0x7fffffffLL || (long long)max_pages * page_size > 0x7fffffffLL)
+    if ((long long)n_pages * page_size * heads_kv > 0x7fffffffLL || (long long)max_pages * page_size > 0x40000000LL)
         return STREE_ERR_UNSUPPORTED;
     if (batch == 0) return STREE_OK;
     if (!k_pages || !v_pages || !table || (cache == STREE_E4M3) != (k_scales != nullptr) ||

@@ -46,16 +46,17 @@ stree_status check_cache(const void *k_pages, const void *v_pages, const void *k
 namespace {
 
 constexpr int kD = kCacheDim;
-constexpr int kBlk = 64;                       // positions per block
-constexpr int kComputeWarps = 4;               // 16 positions each
+constexpr int kComputeWarps = 4;
+// Positions per block: 16 for each warp, 32 with 8-bit pages, where the work on a position counts
+// more than its bytes (two tiles share a maximum and hide each other's latencies).
+__host__ __device__ constexpr int block_positions(bool e4m3) { return e4m3 ? 128 : 64; }
 constexpr int kThreads = (kComputeWarps + 1) * 32;
 constexpr int kMaxHeads = 16;                  // query heads in a row of blocks
 constexpr int kJoinRow = kD + 4;               // floats of a row in shared memory (no bank conflicts)
 constexpr int kMaxStages = 8;
 
-// CTAs per SM: their warps hide one another's latencies, as many as registers and stages allow.
-__host__ __device__ constexpr int ctas_per_sm(bool e4m3, int nt) { return e4m3 && nt == 1 ? 3 : 2; }
-constexpr int smem_per_cta(int ctas) { return 226 * 1024 / ctas; }
+constexpr int kCtasPerSm = 2;
+constexpr int kSmemPerCta = 226 * 1024 / kCtasPerSm;
 constexpr int kCombineWarps = 16, kCombineThreads = kCombineWarps * 32;
 
 struct PagedArgs {
@@ -68,14 +69,14 @@ struct PagedArgs {
                                                // nonzero: a page out of range)
     int32_t *err;
     int batch, heads_q, heads_kv, group, row_tiles, rows;   // rows: min(group, 16)
-    int n_pages, page_size, max_pages, box_rows, shares, stages;
+    int n_pages, page_size, max_pages, blk, box_rows, shares, stages;   // blk: positions per block
     float scale_log2;
 };
 
 __device__ __forceinline__ int blocks_of(const PagedArgs &a, int b)
 {
     const int n = min(max(__ldg(a.lens + b), 0), a.max_pages * a.page_size);
-    return (n + kBlk - 1) / kBlk;
+    return (n + a.blk - 1) / a.blk;
 }
 
 __device__ __forceinline__ long long share_begin(long long total, int c, int shares) { return total * c / shares; }
@@ -146,18 +147,19 @@ struct Stage {                                 // offsets inside a stage of the 
 template <bool kE4m3>
 __host__ __device__ constexpr Stage stage_layout()
 {
-    // 8-bit pages: [64][128 B] tiles and 64 scale bytes each; bf16: two 64-column halves.
-    return kE4m3 ? Stage{0, 8192, 16384, 16384 + 64, 16384 + 1024} : Stage{0, 16384, 0, 0, 32768};
+    // 8-bit pages: [128][128 B] tiles and 128 scale bytes each; bf16: [64] rows, two 64-column halves.
+    return kE4m3 ? Stage{0, 16384, 32768, 32768 + 128, 32768 + 1024} : Stage{0, 16384, 0, 0, 32768};
 }
 
 // NT: tiles of eight query heads in a row of blocks.
 template <bool kE4m3, int NT>
-__global__ void __launch_bounds__(kThreads, ctas_per_sm(kE4m3, NT))
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
 paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                        const PagedArgs a)
 {
     constexpr Stage L = stage_layout<kE4m3>();
-    constexpr int kHeads = 8 * NT;
+    constexpr int kHeads = 8 * NT, kBlk = block_positions(kE4m3), KT = kBlk / 64;   // KT: tiles of 16 positions a warp
+    constexpr int kEighths = kBlk / 8;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ uint64_t bars[2 * kMaxStages];
     __shared__ int tmp[33], found[2];
@@ -206,7 +208,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
 
     if (tid == 0) {
         for (int s = 0; s < a.stages; ++s) {
-            ptx::mbar_init(full(s), kE4m3 ? 1 + 16 : 1);
+            ptx::mbar_init(full(s), kE4m3 ? 1 + 2 * kEighths : 1);
             ptx::mbar_init(empty(s), kComputeWarps);
         }
         ptx::fence_mbar_init();
@@ -235,10 +237,10 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
             ptx::prefetch_tensormap(&tm_k);
             ptx::prefetch_tensormap(&tm_v);
         }
-        // Lane i (mod 8) follows positions 8 i .. 8 i + 7 of the block (an eighth lies in one page): their
-        // page's place in the table and row in the page, moved on by 64 positions without a
+        // Lane i (mod the block's eighths) follows positions 8 i .. 8 i + 7 of the block (an eighth lies in one page): their
+        // page's place in the table and row in the page, moved on by a block without a
         // division (the page ids of one block ahead are in flight while a block is issued).
-        const int mine8 = (lane & 7) * 8, step_p = kBlk / a.page_size, step_r = kBlk % a.page_size;
+        const int mine8 = (lane & (kEighths - 1)) * 8, step_p = kBlk / a.page_size, step_r = kBlk % a.page_size;
         const int first_p = mine8 / a.page_size, first_r = mine8 % a.page_size;
         int at_p = (blk * kBlk + mine8) / a.page_size, at_r = (blk * kBlk + mine8) % a.page_size;
         int n = min(max(__ldg(a.lens + b), 0), a.max_pages * a.page_size);
@@ -272,7 +274,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
                 id = lookup();
             }
             if (lap > 0 && !wait_warp(&aborted, empty(stage), lap - 1, 1)) break;
-            const int eighth = (lane * (a.box_rows / 8)) & 7;   // of the box that this lane issues
+            const int eighth = (lane * (a.box_rows / 8)) & (kEighths - 1);   // of the box that this lane issues
             const int box_id = __shfl_sync(0xffffffffu, cid, eighth), box_row = __shfl_sync(0xffffffffu, crow, eighth);
             const bool mine = lane < boxes && box_id >= 0;
             const uint32_t n_boxes = __popc(__ballot_sync(0xffffffffu, mine));
@@ -293,11 +295,11 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
                     ptx::tma_load_2d(at + L.v + 8192, &tm_v, 64, row, fb);
                 }
             }
-            if (kE4m3 && lane < 16) {
-                // Lanes 0-7 the eighths of the key scales, 8-15 of the value scales.
+            if (kE4m3) {
+                // Half the lanes the eighths of the key scales, half of the value scales.
                 if (cid >= 0)
-                    ptx::cp_async8(base + (lane < 8 ? L.ks : L.vs) + mine8,
-                                   (lane < 8 ? a.k_scales : a.v_scales) + ((size_t)cid * a.heads_kv + chead) * a.page_size + crow);
+                    ptx::cp_async8(base + (lane < kEighths ? L.ks : L.vs) + mine8,
+                                   (lane < kEighths ? a.k_scales : a.v_scales) + ((size_t)cid * a.heads_kv + chead) * a.page_size + crow);
                 asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(fb) : "memory");
             }
             if (++stage == a.stages) {
@@ -384,30 +386,34 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
             if (!(run = wait_warp(&aborted, full(s), phase, 10))) break;
             any_bad |= bad[s];
             const uint32_t base = ptx::smem_u32(smem) + s * L.bytes;
-            const int key0 = warp * 16, valid = n - (blk * kBlk + key0);   // positions of this warp that exist
+            const int key0 = warp * 16 * KT, valid = n - (blk * kBlk + key0);   // positions of this warp that exist
             if (valid > 0) {
-                const bool tail = valid < 16;
-                // Scores: keys r4, r4 + 8 by heads 2 t4, 2 t4 + 1.
-                float sc[NT][4];
+                const bool tail = valid < 16 * KT;
+                // Scores: keys r4, r4 + 8 of each 16 by heads 2 t4, 2 t4 + 1.
+                float sc[KT][NT][4];
 #pragma unroll
-                for (int t = 0; t < NT; ++t) sc[t][0] = sc[t][1] = sc[t][2] = sc[t][3] = 0.f;
+                for (int u = 0; u < KT; ++u)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) sc[u][t][0] = sc[u][t][1] = sc[u][t][2] = sc[u][t][3] = 0.f;
                 // Tiles of eight keys by 16 bytes: keys 0-7 and 8-15 of a chunk, then of the next.
                 const int krow = key0 + (lane & 15), ksw = krow & 7;
                 const uint32_t kaddr = base + L.k + krow * 128, vaddr = base + L.v;
                 if (kE4m3) {
 #pragma unroll
-                    for (int kk = 0; kk < 8; kk += 2) {
-                        uint32_t r[4];
-                        ldsm4(kaddr + (((kk + (lane >> 4)) ^ ksw) << 4), r);
+                    for (int kk = 0; kk < 8; kk += 2)
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            uint32_t k[4];
-                            e4m3x4_to_f16(r[2 * j], k[0], k[2]);
-                            e4m3x4_to_f16(r[2 * j + 1], k[1], k[3]);
+                        for (int u = 0; u < KT; ++u) {
+                            uint32_t r[4];
+                            ldsm4(kaddr + u * 2048 + (((kk + (lane >> 4)) ^ ksw) << 4), r);
 #pragma unroll
-                            for (int t = 0; t < NT; ++t) mma16816<true>(sc[t], k, qf[t][kk + j][0], qf[t][kk + j][1]);
+                            for (int j = 0; j < 2; ++j) {
+                                uint32_t k[4];
+                                e4m3x4_to_f16(r[2 * j], k[0], k[2]);
+                                e4m3x4_to_f16(r[2 * j + 1], k[1], k[3]);
+#pragma unroll
+                                for (int t = 0; t < NT; ++t) mma16816<true>(sc[u][t], k, qf[t][kk + j][0], qf[t][kk + j][1]);
+                            }
                         }
-                    }
                 } else {
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk) {
@@ -415,32 +421,43 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
                         const int chunk = kk * 2 + (lane >> 4);
                         ldsm4(kaddr + (chunk >> 3) * 8192 + (((chunk & 7) ^ ksw) << 4), r);
 #pragma unroll
-                        for (int t = 0; t < NT; ++t) mma16816<false>(sc[t], r, qf[t][kk][0], qf[t][kk][1]);
+                        for (int t = 0; t < NT; ++t) mma16816<false>(sc[0][t], r, qf[t][kk][0], qf[t][kk][1]);
                     }
                 }
-                float kf[2] = {1.f, 1.f}, ve[2] = {0.f, 0.f};   // a key's scale, log2 of a value's
-                if (kE4m3) {
-                    const uint8_t *sb = smem + s * L.bytes + key0 + r4;
+                float kf[KT][2], ve[KT][2];    // a key's scale, log2 of a value's
+#pragma unroll
+                for (int u = 0; u < KT; ++u)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        kf[j] = power_of_two(sb[L.ks + 8 * j]);
-                        ve[j] = __uint_as_float(0x4b000000u | sb[L.vs + 8 * j]) - 8388735.f;   // 2^23 + byte, less 2^23 + 127
+                        kf[u][j] = 1.f;
+                        ve[u][j] = 0.f;
+                        if (kE4m3) {
+                            const uint8_t *sb = smem + s * L.bytes + key0 + 16 * u + 8 * j + r4;
+                            kf[u][j] = power_of_two(sb[L.ks]);
+                            ve[u][j] = __uint_as_float(0x4b000000u | sb[L.vs]) - 8388735.f;   // 2^23 + byte, less 2^23 + 127
+                        }
                     }
-                }
-                uint32_t pf[NT][2];
+                uint32_t pf[KT][NT][2];
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        sc[t][e] *= kE4m3 ? qs[t][e & 1] * kf[e >> 1] : qs[t][e & 1];
-                        if (tail && r4 + 8 * (e >> 1) >= valid) sc[t][e] = -INFINITY;
-                    }
+                    for (int u = 0; u < KT; ++u)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            sc[u][t][e] *= kE4m3 ? qs[t][e & 1] * kf[u][e >> 1] : qs[t][e & 1];
+                            if (tail && 16 * u + 8 * (e >> 1) + r4 >= valid) sc[u][t][e] = -INFINITY;
+                        }
                     // Running maxima of the scores and, for the output, of the scores with the values' scales.
                     float mn[2], rn[2];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        mn[i] = fmaxf(sc[t][i], sc[t][2 + i]);
-                        rn[i] = fmaxf(sc[t][i] + ve[0], sc[t][2 + i] + ve[1]);
+                        mn[i] = fmaxf(sc[0][t][i], sc[0][t][2 + i]);
+                        rn[i] = fmaxf(sc[0][t][i] + ve[0][0], sc[0][t][2 + i] + ve[0][1]);
+#pragma unroll
+                        for (int u = 1; u < KT; ++u) {
+                            mn[i] = fmaxf(mn[i], fmaxf(sc[u][t][i], sc[u][t][2 + i]));
+                            rn[i] = fmaxf(rn[i], fmaxf(sc[u][t][i] + ve[u][0], sc[u][t][2 + i] + ve[u][1]));
+                        }
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1) {
                             mn[i] = fmaxf(mn[i], __shfl_xor_sync(0xffffffffu, mn[i], d));
@@ -467,40 +484,43 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
                     const float m0 = m[t][0] == -INFINITY ? 0.f : m[t][0], m1 = m[t][1] == -INFINITY ? 0.f : m[t][1];
                     const float r0 = ref[t][0] == -INFINITY ? 0.f : ref[t][0], r1 = ref[t][1] == -INFINITY ? 0.f : ref[t][1];
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const float p0 = ptx::ex2_approx(sc[t][2 * j] - m0), p1 = ptx::ex2_approx(sc[t][2 * j + 1] - m1);
-                        l[t][0] += p0;
-                        l[t][1] += p1;
-                        pf[t][j] = transpose8(kE4m3 ? pack_half(ptx::ex2_approx(sc[t][2 * j] + (ve[j] - r0)),
-                                                                ptx::ex2_approx(sc[t][2 * j + 1] + (ve[j] - r1)))
-                                                    : pack_bf16(p0, p1));
-                    }
+                    for (int u = 0; u < KT; ++u)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const float s0 = sc[u][t][2 * j], s1 = sc[u][t][2 * j + 1];
+                            const float p0 = ptx::ex2_approx(s0 - m0), p1 = ptx::ex2_approx(s1 - m1);
+                            l[t][0] += p0;
+                            l[t][1] += p1;
+                            pf[u][t][j] = transpose8(kE4m3 ? pack_half(ptx::ex2_approx(s0 + (ve[u][j] - r0)), ptx::ex2_approx(s1 + (ve[u][j] - r1)))
+                                                           : pack_bf16(p0, p1));
+                        }
                 }
                 // Positions past the end hold anything: their value rows count as zero.
-                const uint32_t keep0 = (2 * t4 < valid ? 0xffffu : 0u) | (2 * t4 + 1 < valid ? 0xffff0000u : 0u);
-                const uint32_t keep1 = (2 * t4 + 8 < valid ? 0xffffu : 0u) | (2 * t4 + 9 < valid ? 0xffff0000u : 0u);
+                auto keep = [&](int key) { return (key < valid ? 0xffffu : 0u) | (key + 1 < valid ? 0xffff0000u : 0u); };
                 if (kE4m3) {
                     // A thread gets columns 2 r4, 2 r4 + 1 of keys 2 t4, 2 t4 + 1: the even columns are
                     // the operand's rows 0-7, the odd ones its rows 8-15.
 #pragma unroll
-                    for (int c = 0; c < 8; c += 2) {
-                        uint32_t r[4];
-                        ldsm4_t(vaddr + krow * 128 + (((c + (lane >> 4)) ^ ksw) << 4), r);
+                    for (int c = 0; c < 8; c += 2)
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            uint32_t v[4];
-                            e4m3x4_to_f16(__byte_perm(r[2 * j], 0, 0x3120), v[0], v[1]);
-                            e4m3x4_to_f16(__byte_perm(r[2 * j + 1], 0, 0x3120), v[2], v[3]);
-                            if (tail) {
-                                v[0] &= keep0;
-                                v[1] &= keep0;
-                                v[2] &= keep1;
-                                v[3] &= keep1;
+                        for (int u = 0; u < KT; ++u) {
+                            uint32_t r[4];
+                            ldsm4_t(vaddr + krow * 128 + u * 2048 + (((c + (lane >> 4)) ^ ksw) << 4), r);
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                uint32_t v[4];
+                                e4m3x4_to_f16(__byte_perm(r[2 * j], 0, 0x3120), v[0], v[1]);
+                                e4m3x4_to_f16(__byte_perm(r[2 * j + 1], 0, 0x3120), v[2], v[3]);
+                                if (tail) {
+                                    v[0] &= keep(16 * u + 2 * t4);
+                                    v[1] &= keep(16 * u + 2 * t4);
+                                    v[2] &= keep(16 * u + 2 * t4 + 8);
+                                    v[3] &= keep(16 * u + 2 * t4 + 8);
+                                }
+#pragma unroll
+                                for (int t = 0; t < NT; ++t) mma16816<true>(acc[t][c + j], v, pf[u][t][0], pf[u][t][1]);
                             }
-#pragma unroll
-                            for (int t = 0; t < NT; ++t) mma16816<true>(acc[t][c + j], v, pf[t][0], pf[t][1]);
                         }
-                    }
                 } else {
                     // Tiles: keys 0-7 of two chunks of eight columns, then keys 8-15.
                     const int vrow = key0 + (lane & 7) + ((lane >> 4) << 3);
@@ -510,13 +530,13 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
                         const int chunk = 2 * c + ((lane >> 3) & 1);
                         ldsm4_t(vaddr + (chunk >> 3) * 8192 + vrow * 128 + (((chunk & 7) ^ (vrow & 7)) << 4), v);
                         if (tail) {
-                            v[0] &= keep0;
-                            v[1] &= keep0;
-                            v[2] &= keep1;
-                            v[3] &= keep1;
+                            v[0] &= keep(2 * t4);
+                            v[1] &= keep(2 * t4);
+                            v[2] &= keep(2 * t4 + 8);
+                            v[3] &= keep(2 * t4 + 8);
                         }
 #pragma unroll
-                        for (int t = 0; t < NT; ++t) mma16816<false>(acc[t][c], v, pf[t][0], pf[t][1]);
+                        for (int t = 0; t < NT; ++t) mma16816<false>(acc[t][c], v, pf[0][t][0], pf[0][t][1]);
                     }
                 }
             }
@@ -690,13 +710,9 @@ cudaError_t prepare(int *sms)
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
     std::lock_guard<std::mutex> lock(g_mutex);
     if (!g_sms[dev]) {
-        const auto set = [](auto *f, bool e4m3, int nt) {
-            return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_per_cta(ctas_per_sm(e4m3, nt)));
-        };
-        if ((e = set(paged_attention_kernel<false, 1>, false, 1)) != cudaSuccess ||
-            (e = set(paged_attention_kernel<false, 2>, false, 2)) != cudaSuccess ||
-            (e = set(paged_attention_kernel<true, 1>, true, 1)) != cudaSuccess ||
-            (e = set(paged_attention_kernel<true, 2>, true, 2)) != cudaSuccess)
+        const auto set = [](auto *f) { return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerCta); };
+        if ((e = set(paged_attention_kernel<false, 1>)) != cudaSuccess || (e = set(paged_attention_kernel<false, 2>)) != cudaSuccess ||
+            (e = set(paged_attention_kernel<true, 1>)) != cudaSuccess || (e = set(paged_attention_kernel<true, 2>)) != cudaSuccess)
             return e;
         int n = 0;
         if ((e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
@@ -724,7 +740,7 @@ extern "C" stree_status stree_paged_attention_workspace_size(int heads_q, int he
     int sms = 0;
     if (prepare(&sms) != cudaSuccess) return STREE_ERR_CUDA;
     const int group = heads_q / heads_kv;
-    *bytes = paged_ws(3 * sms, group < kMaxHeads ? group : kMaxHeads);
+    *bytes = paged_ws(kCtasPerSm * sms, group < kMaxHeads ? group : kMaxHeads);
     return STREE_OK;
 }
 
@@ -750,20 +766,20 @@ extern "C" stree_status stree_paged_attention(const void *q, const void *k_pages
     const int nt = a.group <= 8 ? 1 : 2;
     a.rows = a.group < 8 * nt ? a.group : 8 * nt;
     a.row_tiles = (a.group + 8 * nt - 1) / (8 * nt);
-    const long long blocks = ((long long)max_pages * page_size + kBlk - 1) / kBlk;
+    const bool e4m3 = cache_dtype == STREE_E4M3;
+    a.blk = block_positions(e4m3);
+    const long long blocks = ((long long)max_pages * page_size + a.blk - 1) / a.blk;
     if (blocks * batch > 0x7fffffffLL || (long long)batch * heads_kv * a.row_tiles > 0x7fffffffLL)
         return STREE_ERR_UNSUPPORTED;
     int sms = 0;
     if (prepare(&sms) != cudaSuccess) return STREE_ERR_CUDA;
     // As many shares as the SMs hold CTAs, and no more than there can be blocks.
     const long long most = blocks * batch * heads_kv * a.row_tiles;
-    const bool e4m3 = cache_dtype == STREE_E4M3;
-    const int ctas = ctas_per_sm(e4m3, nt);
-    a.shares = (int)(most < (long long)ctas * sms ? most : (long long)ctas * sms);
+    a.shares = (int)(most < (long long)kCtasPerSm * sms ? most : (long long)kCtasPerSm * sms);
     const size_t need = paged_ws(a.shares, a.rows);
     if (workspace_bytes < need) return STREE_ERR_INVALID_ARG;
     a.box_rows = 8;
-    while (a.box_rows < kBlk && page_size % (2 * a.box_rows) == 0) a.box_rows *= 2;
+    while (a.box_rows < 64 && page_size % (2 * a.box_rows) == 0) a.box_rows *= 2;
     const long long rows = (long long)n_pages * heads_kv * page_size;
     CUtensorMap m_k, m_v;
     if (!encode_rows(&m_k, k_pages, e4m3, rows, a.box_rows) || !encode_rows(&m_v, v_pages, e4m3, rows, a.box_rows))
@@ -786,7 +802,7 @@ extern "C" stree_status stree_paged_attention(const void *q, const void *k_pages
     a.scale_log2 = scale * 1.4426950408889634f;
     const int stage = e4m3 ? stage_layout<true>().bytes : stage_layout<false>().bytes;
     const int join = kComputeWarps * a.rows * kJoinRow * (int)sizeof(float), slack = 1024, fixed = 3072;
-    a.stages = (smem_per_cta(ctas) - join - slack - fixed) / stage;
+    a.stages = (kSmemPerCta - join - slack - fixed) / stage;
     if (a.stages > kMaxStages) a.stages = kMaxStages;
     const size_t smem = (size_t)a.stages * stage + join + slack;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
