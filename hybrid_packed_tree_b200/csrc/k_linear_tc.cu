@@ -287,16 +287,16 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         } else if (warp == 2) {
             // ------------------------------------------------------------ gates
             double total[2] = {0.0, 0.0};
-            float al[NH][4], be[NH][4];        // of tokens lane + 32 J
+            float4 al[NH], be[NH];             // of tokens 4 lane .. 4 lane + 3
             auto fetch = [&](int i) {
 #pragma unroll
                 for (int h = 0; h < NH; ++h)
 #pragma unroll
-                    for (int J = 0; J < 4; ++J) {
-                        const int t = (c0 + i) * kC + J * 32 + lane;
+                    for (int e = 0; e < 4; ++e) {
+                        const int t = (c0 + i) * kC + lane * 4 + e;
                         const size_t at = (size_t)(seq.x + t) * a.heads_v + head0 + h;
-                        al[h][J] = t < len ? __ldg(a.alpha + at) : 1.f;
-                        be[h][J] = t < len ? (a.beta ? __ldg(a.beta + at) : 1.f) : 0.f;   // weight zero past the end
+                        (&al[h].x)[e] = t < len ? __ldg(a.alpha + at) : 1.f;
+                        (&be[h].x)[e] = t < len ? (a.beta ? __ldg(a.beta + at) : 1.f) : 0.f;   // weight zero past the end
                     }
             };
             if (n > 0) fetch(0);
@@ -304,38 +304,43 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             for (int i = 0; i < n; ++i) {
                 if (i >= 2 && !warp_wait(B_GE + (i & 1), (uint32_t)((i >> 1) - 1), 30)) break;
                 Gates &G = gates[i & 1];
-                // A block of 32 tokens at a time, last to first: `after` is the log decay from its end
-                // to the chunk's end.
-                double after[2] = {0.0, 0.0};
-#pragma unroll 1
-                for (int x = 4 * NH - 1; x >= 0; --x) {
-                    const int h = NH == 2 ? x & 1 : 0, J = NH == 2 ? x >> 1 : x;
-                    float alpha = al[0][0], beta = be[0][0];
 #pragma unroll
-                    for (int y = 1; y < 4 * NH; ++y) {
-                        alpha = x == y ? al[NH == 2 ? y & 1 : 0][NH == 2 ? y >> 1 : y] : alpha;
-                        beta = x == y ? be[NH == 2 ? y & 1 : 0][NH == 2 ? y >> 1 : y] : beta;
+                for (int h = 0; h < NH; ++h) {
+                    // One scan over the lanes, four tokens each; eight lanes are a block of 32 tokens.  (Four
+                    // scans of 32 tokens, in a loop to save code, made this warp the slowest role.)
+                    double L[4], sum = 0.0;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        sum += (double)fmaxf(log2f((&al[h].x)[e]), kLogZero);
+                        L[e] = sum;
                     }
-                    const float lg = log2f(alpha);
-                    double L = (double)(lg < kLogZero ? kLogZero : lg);
+                    double scan = sum;
 #pragma unroll
                     for (int d = 1; d < 32; d <<= 1) {
-                        const double u = __shfl_up_sync(0xffffffffu, L, d);
-                        if (lane >= d) L += u;
+                        const double u = __shfl_up_sync(0xffffffffu, scan, d);
+                        if (lane >= d) scan += u;
                     }
-                    const double end = __shfl_sync(0xffffffffu, L, 31), rest = h == 0 ? after[0] : after[1];
-                    const int j = J * 32 + lane;
-                    G.rel[h][j] = (float)L;
-                    G.beta[h][j] = beta;
-                    G.fac[h][j] = exp2f((float)(end - L)) * beta;
-                    G.w[h][j] = exp2f((float)(end - L + rest)) * beta;
-                    if (lane == 0) G.after[h][J] = rest;
-                    if (h == 0) after[0] += end;
-                    else after[1] += end;
+                    const double before = scan - sum, all = __shfl_sync(0xffffffffu, scan, 31);
+                    const double end = __shfl_sync(0xffffffffu, scan, lane | 7);
+                    const double prev = __shfl_sync(0xffffffffu, scan, max((lane & 24) - 1, 0));
+                    const double start = lane < 8 ? 0.0 : prev;
+                    if ((lane & 7) == 7) G.after[h][lane >> 3] = all - scan;
+                    float4 rel, fac, w;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const double Le = before + L[e];
+                        const float beta = (&be[h].x)[e];
+                        (&rel.x)[e] = (float)(Le - start);
+                        (&fac.x)[e] = ptx::ex2_approx((float)(end - Le)) * beta;
+                        (&w.x)[e] = exp2f((float)(all - Le)) * beta;
+                    }
+                    *reinterpret_cast<float4 *>(&G.rel[h][lane * 4]) = rel;
+                    *reinterpret_cast<float4 *>(&G.fac[h][lane * 4]) = fac;
+                    *reinterpret_cast<float4 *>(&G.w[h][lane * 4]) = w;
+                    *reinterpret_cast<float4 *>(&G.beta[h][lane * 4]) = be[h];
+                    if (lane == 0) G.all[h] = all;
+                    total[h] += all;
                 }
-                if (lane < NH) G.all[lane] = lane == 0 ? after[0] : after[1];
-                total[0] += after[0];
-                total[1] += after[1];
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(bar(B_GF + (i & 1)));
                 if (i + 1 < n) fetch(i + 1);
