@@ -21,7 +21,7 @@
 // is a difference of L's taken before it is rounded.
 //
 // Warp roles (16 warps, bounded mbarrier waits): a producer (TMA: K, Q, V tiles of 32 KB into a
-// ring of five), the MMA issuer, a gate warp (L, w and the factors of P, one chunk ahead),
+// ring of five), the MMA issuer, two gate warps (L, w and the factors of P, a chunk in turn),
 // four warps for P and O (a token per thread), and eight for the state (a row of S per
 // thread and half of its columns): they read V by columns and put the three parts of w v into tensor
 // memory as the A operand, 32 tokens at a time in two alternating buffers, then add the product
@@ -52,12 +52,17 @@ constexpr int kMaxDevices = 64;
 
 enum Bars {
     B_F = 0, B_E = B_F + kSlots, B_GF = B_E + kSlots, B_GE = B_GF + 2, B_SF = B_GE + 2, B_PF, B_OQ, B_OF, B_OE, B_SOP,
-    B_WF, B_WE = B_WF + 2, B_DF = B_WE + 2, B_DRAIN, kBars
+    B_WF, B_WE = B_WF + 4, B_DF = B_WE + 4, B_DRAIN = B_DF + 2, kBars
 };
 
 // Tensor memory: Q K^T, then P over it (of every 32 columns, 16 for a head); O; the state's
 // update; the parts of w v.
 constexpr uint32_t kColP = 0, kColO = 128, kColD = 256, kColW = 384;
+
+// The state-only launch has no P and no O: their columns hold two more of the parts' buffers and a
+// second one for the update.
+__device__ __forceinline__ uint32_t state_col_w(int s) { return s < 2 ? kColP + s * 64 : kColW + (s - 2) * 64; }
+__device__ __forceinline__ uint32_t state_col_d(int i) { return i & 1 ? kColO : kColD; }
 
 struct Gates {                                 // of one chunk, per head
     float rel[2][kC];                          // L_i less L at the end of the block before i's
@@ -74,7 +79,7 @@ struct TcArgs {
     __nv_bfloat16 *o;
     float *S_new;
     float *seg_state;                          // [item][segments][128][128]: S0, then every segment's but the last
-    double *seg_log;                           // [item][segments - 1][2]
+    double *seg_log;                           // [item][segments - 1][even, odd chunks][2]
     int32_t *err;
     int total, batch, heads_v, heads_k, per_seq, segments;   // per_seq: 128-column items of a sequence
 };
@@ -155,10 +160,10 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         ptx::prefetch_tensormap(&tm_k);
         ptx::prefetch_tensormap(&tm_v);
         for (int i = 0; i < kBars; ++i) {
-            const int count = i == B_PF || i == B_OE || i == B_WF || i == B_WF + 1 ? 4
-                              : i == B_SOP                                         ? 8
-                              : i == B_GE || i == B_GE + 1                         ? (kState ? 8 : 12)
-                                                                                   : 1;
+            const int count = i == B_PF || i == B_OE || (i >= B_WF && i < B_WE) ? 4
+                              : i == B_SOP                                       ? 8
+                              : i == B_GE || i == B_GE + 1                       ? 12
+                                                                                 : 1;
             ptx::mbar_init(bar(i), count);
         }
         ptx::fence_mbar_init();
@@ -176,6 +181,59 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     auto load_k = [&](int i) { return kLoads * i; };
     auto load_q = [&](int i) { return kLoads * i + 1; };
     auto load_v = [&](int i) { return kLoads * i + kLoads - 1; };
+
+    // Tokens 32 s .. 32 s + 31 of chunk i as w v, for the value columns of this warp's quarter of the lanes, in
+    // three parts of 16 columns from `col` on.
+    auto form = [&](int i, int s, uint32_t col) {
+        const Gates &G = gates[i & 1];
+        const int x = load_v(i), valid = min(kC, len - (c0 + i) * kC), quad = warp & 3;
+        const int h = NH == 2 ? quad >> 1 : 0;
+        // This lane's row address for ldmatrix: token lane % 8 of eight, the warp's columns 8 (lane / 8) ..
+        const uint32_t v = ring + (x % kSlots) * kTile + (quad >> 1) * kHalf + (lane & 7) * 128 +
+                           ((((quad & 1) * 4 + (lane >> 3)) ^ (lane & 7)) << 4);
+        const uint32_t t_w = tmem + col + ((uint32_t)(quad * 32) << 16);
+#pragma unroll 1
+        for (int z = 0; z < 2; ++z) {  // 16 tokens
+            // Transposed 8 x 8 tiles: a register is two tokens (2 (lane % 4), + 1) of column lane / 4.
+            const int t0 = s * 32 + z * 16, t = t0 + (lane & 3) * 2;
+            uint32_t raw[2][4];
+            ldsm4_t(v + t0 * 128, raw[0]);
+            ldsm4_t(v + t0 * 128 + 1024, raw[1]);
+            const float2 w[2] = {*reinterpret_cast<const float2 *>(&G.w[h][t]), *reinterpret_cast<const float2 *>(&G.w[h][t + 8])};
+            float2 y[2][4];
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) y[e][c] = ptx::fmul2(w[e], make_float2(low(raw[e][c]), high(raw[e][c])));
+            if (t0 + 16 > valid)       // another sequence's rows
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        y[e][c].x = t + 8 * e < valid ? y[e][c].x : 0.f;
+                        y[e][c].y = t + 8 * e + 1 < valid ? y[e][c].y : 0.f;
+                    }
+            // Three parts of eight bits each, cut off rather than rounded: their sum is exact.
+#pragma unroll
+            for (int part = 0; part < 3; ++part) {
+                uint32_t p[2][4];
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t bx = __float_as_uint(y[e][c].x), by = __float_as_uint(y[e][c].y);
+                        p[e][c] = __byte_perm(bx, by, 0x7632);
+                        if (part < 2)
+                            y[e][c] = ptx::ffma2(make_float2(low(p[e][c]), high(p[e][c])), make_float2(-1.f, -1.f), y[e][c]);
+                    }
+                ptx::tmem_st16x8(t_w + part * 16 + z * 8, p[0][0], p[0][1], p[1][0], p[1][1]);
+                ptx::tmem_st16x8(t_w + (16u << 16) + part * 16 + z * 8, p[0][2], p[0][3], p[1][2], p[1][3]);
+            }
+        }
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        __syncwarp();
+    };
 
     int loads = 0;
     if (warp < 4) {
@@ -203,6 +261,47 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             auto release = [&](int x) {        // a slot that another load will use
                 if (x + kSlots < kLoads * n) ptx::mma_commit(bar(B_E + x % kSlots));
             };
+            // Tokens 64 u .. 64 u + 63 of chunk i into the state's update: 32 at a time, three parts of two
+            // steps each.
+            auto update = [&](int i, int u, uint64_t d_kt) -> bool {
+                if (!warp_wait(B_WF, (uint32_t)(2 * i + u), 14) || !warp_wait(B_WF + 1, (uint32_t)(2 * i + u), 17)) return false;
+                if (ptx::elect_one()) {
+                    ptx::tc_fence_after();
+#pragma unroll 1
+                    for (int s = 0; s < 2; ++s) {
+#pragma unroll
+                        for (int part = 0; part < 3; ++part)
+#pragma unroll
+                            for (int kk = 0; kk < 2; ++kk)
+                                ptx::mma_f16_ta(tmem + kColD, tmem + kColW + s * 64 + part * 16 + kk * 8,
+                                                ptx::desc_at(d_kt, (4 * u + 2 * s + kk) * 2048), id_mn, (u | s | part | kk) != 0);
+                        ptx::mma_commit(bar(B_WE + s));
+                    }
+                }
+                __syncwarp();
+                return true;
+            };
+            // The same of a whole chunk in the state-only launch: a buffer for each 32 tokens, and two for the
+            // update (the tokens that the state warps form come first: they have read the last but one).
+            auto update_all = [&](int i, uint64_t d_kt) -> bool {
+#pragma unroll 1
+                for (int e = 0; e < 4; ++e) {
+                    const int s = (e + 2) & 3;
+                    if (!warp_wait(B_WF + s, (uint32_t)i, 14) || (e == 0 && !warp_wait(B_WF + 3, (uint32_t)i, 17))) return false;
+                    if (ptx::elect_one()) {
+                        ptx::tc_fence_after();
+#pragma unroll
+                        for (int part = 0; part < 3; ++part)
+#pragma unroll
+                            for (int kk = 0; kk < 2; ++kk)
+                                ptx::mma_f16_ta(tmem + state_col_d(i), tmem + state_col_w(s) + part * 16 + kk * 8,
+                                                ptx::desc_at(d_kt, (2 * s + kk) * 2048), id_mn, (e | part | kk) != 0);
+                        ptx::mma_commit(bar(B_WE + s));
+                    }
+                    __syncwarp();
+                }
+                return true;
+            };
             bool ok = true;
 #pragma unroll 1
             for (int i = 0; i < n && ok; ++i) {
@@ -224,7 +323,16 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         ptx::mma_commit(bar(B_SF));
                     }
                     __syncwarp();
-                    // Q S^T, once the state's copy is there and the last chunk's O has been read.
+                }
+                // The state's update: tokens 0-63 now, the others behind Q S^T, which waits for the last
+                // chunk's O to be read.  The first product overwrites the last chunk's update, so both
+                // halves of the state warps have to have read that: they hand over w v after it.
+                if (kState) {
+                    if (!(ok = update_all(i, d_kt))) break;
+                } else if (!(ok = update(i, 0, d_kt))) {
+                    break;
+                }
+                if (!kState) {
                     if (!(ok = warp_wait(B_SOP, (uint32_t)i, 12)) || (i > 0 && !(ok = warp_wait(B_OE, (uint32_t)(i - 1), 13)))) break;
                     if (ptx::elect_one()) {
                         ptx::tc_fence_after();
@@ -236,29 +344,10 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         release(load_q(i));
                     }
                     __syncwarp();
-                } else if (i > 0 && !(ok = warp_wait(B_SOP, (uint32_t)(i - 1), 12))) {
-                    break;                     // the last update has been read
                 }
-                // The state's update: 32 tokens at a time, three parts of two steps each.
-#pragma unroll 1
-                for (int s = 0; s < 4 && ok; ++s) {
-                    if (!(ok = warp_wait(B_WF + (s & 1), (uint32_t)(2 * i + (s >> 1)), 14))) break;
-                    if (ptx::elect_one()) {
-                        ptx::tc_fence_after();
-#pragma unroll
-                        for (int part = 0; part < 3; ++part)
-#pragma unroll
-                            for (int kk = 0; kk < 2; ++kk)
-                                ptx::mma_f16_ta(tmem + kColD, tmem + kColW + (s & 1) * 64 + part * 16 + kk * 8,
-                                                ptx::desc_at(d_kt, (2 * s + kk) * 2048), id_mn,
-                                                (s | part | kk) != 0);
-                        ptx::mma_commit(bar(B_WE + (s & 1)));
-                    }
-                    __syncwarp();
-                }
-                if (!ok) break;
+                if (!kState && !(ok = update(i, 1, d_kt))) break;
                 if (ptx::elect_one()) {
-                    ptx::mma_commit(bar(B_DF));
+                    ptx::mma_commit(bar(B_DF + (i & 1)));
                     release(load_k(i));
                 }
                 __syncwarp();
@@ -284,8 +373,9 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 }
                 __syncwarp();
             }
-        } else if (warp == 2) {
+        } else {
             // ------------------------------------------------------------ gates
+            const int gw = warp - 2;           // warp 2 the even chunks, warp 3 the odd ones
             double total[2] = {0.0, 0.0};
             float4 al[NH], be[NH];             // of tokens 4 lane .. 4 lane + 3
             auto fetch = [&](int i) {
@@ -299,11 +389,11 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         (&be[h].x)[e] = t < len ? (a.beta ? __ldg(a.beta + at) : 1.f) : 0.f;   // weight zero past the end
                     }
             };
-            if (n > 0) fetch(0);
+            if (gw < n) fetch(gw);
 #pragma unroll 1
-            for (int i = 0; i < n; ++i) {
-                if (i >= 2 && !warp_wait(B_GE + (i & 1), (uint32_t)((i >> 1) - 1), 30)) break;
-                Gates &G = gates[i & 1];
+            for (int i = gw; i < n; i += 2) {
+                if (i >= 2 && !warp_wait(B_GE + gw, (uint32_t)((i >> 1) - 1), 30)) break;
+                Gates &G = gates[gw];
 #pragma unroll
                 for (int h = 0; h < NH; ++h) {
                     // One scan over the lanes, four tokens each; eight lanes are a block of 32 tokens.  (Four
@@ -342,14 +432,31 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     total[h] += all;
                 }
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(bar(B_GF + (i & 1)));
-                if (i + 1 < n) fetch(i + 1);
+                if (lane == 0) ptx::mbar_arrive(bar(B_GF + gw));
+                if (i + 2 < n) fetch(i + 2);   // in flight while the other warp's chunk is worked on
             }
-            if (kState && lane < NH) a.seg_log[((size_t)flat * segs + seg) * 2 + lane] = lane == 0 ? total[0] : total[1];
+            if (kState && lane < 2) a.seg_log[((size_t)flat * segs + seg) * 4 + gw * 2 + lane] = lane == 0 ? total[0] : total[1];
         }
     } else if (warp < 8) {
         // ---------------------------------------------------------------- P and O
-        if (!kState) {
+        if (kState) {
+            // These warps form w v of the first 64 tokens.
+#pragma unroll 1
+            for (int i = 0; i < n; ++i) {
+                const int x = load_v(i);
+                if (!warp_wait(B_GF + (i & 1), (uint32_t)(i >> 1), 50) || !warp_wait(B_F + x % kSlots, (uint32_t)(x / kSlots), 51)) break;
+                bool ok = true;
+#pragma unroll 1
+                for (int s = 0; s < 2; ++s) {
+                    if (i > 0 && !(ok = warp_wait(B_WE + s, (uint32_t)(i - 1), 52))) break;
+                    ptx::tc_fence_after();
+                    form(i, s, state_col_w(s));
+                    if (lane == 0) ptx::mbar_arrive(bar(B_WF + s));
+                }
+                if (!ok) break;
+                if (lane == 0) ptx::mbar_arrive(bar(B_GE + (i & 1)));
+            }
+        } else {
             const int quad = warp & 3, r = quad * 32 + lane;
             const uint32_t lanes = (uint32_t)(quad * 32) << 16;
             const uint32_t t_p = tmem + kColP + lanes, t_o = tmem + kColO + lanes;
@@ -490,7 +597,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 #pragma unroll 1
             for (int s = 0; s < seg; ++s) {    // the segments before this one
                 const size_t p = (size_t)flat * (a.segments - 1) + s;
-                const float f = exp2f((float)a.seg_log[p * 2 + h]);
+                const float f = exp2f((float)(a.seg_log[p * 4 + h] + a.seg_log[p * 4 + 2 + h]));
                 const float4 *src = reinterpret_cast<const float4 *>(slots + (size_t)(s + 1) * kC * kC);
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
@@ -503,88 +610,23 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             }
         // The bf16 copy that the next Q S^T reads: row r of this half.
         auto copy_out = [&] {
-            if (!kState) {
-                uint8_t *dst = sop + wg * kHalf + r * 128;
+            uint8_t *dst = sop + wg * kHalf + r * 128;
 #pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    *reinterpret_cast<uint4 *>(dst + ((c ^ (r & 7)) << 4)) =
-                        make_uint4(pack2(st[8 * c], st[8 * c + 1]), pack2(st[8 * c + 2], st[8 * c + 3]),
-                                   pack2(st[8 * c + 4], st[8 * c + 5]), pack2(st[8 * c + 6], st[8 * c + 7]));
-                ptx::fence_proxy_async_smem();
-            }
+            for (int c = 0; c < 8; ++c)
+                *reinterpret_cast<uint4 *>(dst + ((c ^ (r & 7)) << 4)) =
+                    make_uint4(pack2(st[8 * c], st[8 * c + 1]), pack2(st[8 * c + 2], st[8 * c + 3]),
+                               pack2(st[8 * c + 4], st[8 * c + 5]), pack2(st[8 * c + 6], st[8 * c + 7]));
+            ptx::fence_proxy_async_smem();
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar(B_SOP));
         };
-        bool run = true;
-#pragma unroll 1
-        for (int i = 0; i < n; ++i) {
-            if (!kState || i > 0) copy_out();  // Q S^T of the last chunk was issued before its update and is done
-            const Gates &G = gates[i & 1];
-            const int x = load_v(i), valid = min(kC, len - (c0 + i) * kC);
-            if (!(run = warp_wait(B_GF + (i & 1), (uint32_t)(i >> 1), 40) && warp_wait(B_F + x % kSlots, (uint32_t)(x / kSlots), 41))) break;
-            // This lane's row address for ldmatrix: token lane % 8 of eight, the warp's columns 8 (lane / 8) ..
-            const uint32_t v = ring + (x % kSlots) * kTile + (quad >> 1) * kHalf + (lane & 7) * 128 +
-                               ((((quad & 1) * 4 + (lane >> 3)) ^ (lane & 7)) << 4);
-#pragma unroll 1
-            for (int u = 0; u < 2; ++u) {
-                const int s = 2 * u + wg, uses = 2 * i + u;
-                if (uses > 0 && !(run = warp_wait(B_WE + wg, (uint32_t)(uses - 1), 42))) break;
-                ptx::tc_fence_after();
-                const uint32_t t_w = tmem + kColW + wg * 64 + lanes;
-#pragma unroll 1
-                for (int z = 0; z < 2; ++z) {  // 16 tokens
-                    // Transposed 8 x 8 tiles: a register is two tokens (2 (lane % 4), + 1) of column lane / 4.
-                    const int t0 = s * 32 + z * 16, t = t0 + (lane & 3) * 2;
-                    uint32_t raw[2][4];
-                    ldsm4_t(v + t0 * 128, raw[0]);
-                    ldsm4_t(v + t0 * 128 + 1024, raw[1]);
-                    const float2 w[2] = {*reinterpret_cast<const float2 *>(&G.w[h][t]), *reinterpret_cast<const float2 *>(&G.w[h][t + 8])};
-                    float2 y[2][4];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) y[e][c] = ptx::fmul2(w[e], make_float2(low(raw[e][c]), high(raw[e][c])));
-                    if (t0 + 16 > valid)       // another sequence's rows
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                y[e][c].x = t + 8 * e < valid ? y[e][c].x : 0.f;
-                                y[e][c].y = t + 8 * e + 1 < valid ? y[e][c].y : 0.f;
-                            }
-                    // Three parts of eight bits each, cut off rather than rounded: their sum is exact.
-#pragma unroll
-                    for (int part = 0; part < 3; ++part) {
-                        uint32_t p[2][4];
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                const uint32_t bx = __float_as_uint(y[e][c].x), by = __float_as_uint(y[e][c].y);
-                                p[e][c] = __byte_perm(bx, by, 0x7632);
-                                if (part < 2)
-                                    y[e][c] = ptx::ffma2(make_float2(low(p[e][c]), high(p[e][c])), make_float2(-1.f, -1.f), y[e][c]);
-                            }
-                        ptx::tmem_st16x8(t_w + part * 16 + z * 8, p[0][0], p[0][1], p[1][0], p[1][1]);
-                        ptx::tmem_st16x8(t_w + (16u << 16) + part * 16 + z * 8, p[0][2], p[0][3], p[1][2], p[1][3]);
-                    }
-                }
-                ptx::tmem_wait_st();
-                ptx::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(bar(B_WF + wg));
-            }
-            if (!run) break;
-            const float decay = exp2f((float)G.all[h]);
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(bar(B_GE + (i & 1)));
-            if (!(run = warp_wait(B_DF, (uint32_t)i, 43))) break;
-            ptx::tc_fence_after();
+        // S' = decay S + the update in these columns.
+        auto take = [&](float decay, uint32_t col) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 uint32_t d[32];
-                ptx::tmem_ld32(tmem + kColD + wg * 64 + c * 32 + lanes, d);
+                ptx::tmem_ld32(tmem + col + wg * 64 + c * 32 + lanes, d);
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
                     const float2 x = ptx::ffma2(make_float2(decay, decay), make_float2(st[c * 32 + e], st[c * 32 + e + 1]),
@@ -593,6 +635,51 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     st[c * 32 + e + 1] = x.y;
                 }
             }
+        };
+        bool run = true;
+        float decay = 0.f;
+#pragma unroll 1
+        for (int i = 0; i < n + (kState ? 1 : 0); ++i) {
+            const int x = load_v(i);
+            if (kState) {
+                // Chunk i is formed before chunk i - 1 is taken, so that the tensor cores always have work.
+                float next = 0.f;
+                if (i < n) {
+                    if (!(run = warp_wait(B_GF + (i & 1), (uint32_t)(i >> 1), 40) && warp_wait(B_F + x % kSlots, (uint32_t)(x / kSlots), 41) &&
+                                (i == 0 || warp_wait(B_WE + 2 + wg, (uint32_t)(i - 1), 42))))
+                        break;
+                    ptx::tc_fence_after();
+                    form(i, 2 + wg, state_col_w(2 + wg));
+                    if (lane == 0) ptx::mbar_arrive(bar(B_WF + 2 + wg));
+                    next = exp2f((float)gates[i & 1].all[h]);
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(bar(B_GE + (i & 1)));
+                }
+                if (i > 0) {
+                    if (!(run = warp_wait(B_DF + ((i - 1) & 1), (uint32_t)((i - 1) >> 1), 43))) break;
+                    ptx::tc_fence_after();
+                    take(decay, state_col_d(i - 1));
+                }
+                decay = next;
+                continue;
+            }
+            copy_out();                        // Q S^T of the last chunk was issued before its update was done
+            if (!(run = warp_wait(B_GF + (i & 1), (uint32_t)(i >> 1), 40) && warp_wait(B_F + x % kSlots, (uint32_t)(x / kSlots), 41))) break;
+#pragma unroll 1
+            for (int u = 0; u < 2; ++u) {
+                const int s = 2 * u + wg, uses = 2 * i + u;
+                if (uses > 0 && !(run = warp_wait(B_WE + wg, (uint32_t)(uses - 1), 42))) break;
+                ptx::tc_fence_after();
+                form(i, s, kColW + wg * 64);
+                if (lane == 0) ptx::mbar_arrive(bar(B_WF + wg));
+            }
+            if (!run) break;
+            decay = exp2f((float)gates[i & 1].all[h]);
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar(B_GE + (i & 1)));
+            if (!(run = warp_wait(B_DF + (i & 1), (uint32_t)(i >> 1), 43))) break;
+            ptx::tc_fence_after();
+            take(decay, kColD);
         }
         float *dst = kState ? slots + (size_t)(seg + 1) * kC * kC
                             : last && a.S_new ? a.S_new + at : nullptr;
@@ -655,7 +742,7 @@ int segments_for(int batch, int total, int items, int sms)
 
 size_t workspace_for(int items, int segments)
 {
-    return segments > 1 ? (size_t)items * segments * (kC * kC * sizeof(float) + 2 * sizeof(double)) : 0;
+    return segments > 1 ? (size_t)items * segments * (kC * kC * sizeof(float) + 4 * sizeof(double)) : 0;
 }
 
 }  // namespace
@@ -699,7 +786,7 @@ cudaError_t launch_linear_tc(const LinearArgs &l, void *workspace, size_t worksp
     if (!workspace || workspace_bytes < workspace_for(items, a.segments)) a.segments = 1;
     if (a.segments > 1) {
         a.seg_log = static_cast<double *>(workspace);
-        a.seg_state = reinterpret_cast<float *>(a.seg_log + (size_t)items * a.segments * 2);
+        a.seg_state = reinterpret_cast<float *>(a.seg_log + (size_t)items * a.segments * 4);
     }
     CUtensorMap q{}, k{}, v{};
     if (l.total > 0 && (!encode_heads(&q, l.q, l.total, l.heads_k, 1, kC) || !encode_heads(&k, l.k, l.total, l.heads_k, 1, kC) ||
