@@ -22,8 +22,8 @@
 //
 // Warp roles (16 warps, bounded mbarrier waits): a producer (TMA: K, Q, V tiles of 32 KB into a
 // ring of five), the MMA issuer, two gate warps (L, w and the factors of P, a chunk in turn),
-// four warps for P and O (a token per thread), and eight for the state (a row of S per
-// thread and half of its columns): they read V by columns and put the three parts of w v into tensor
+// four warps for P and O (a token per thread), and eight for the state (a row of S per thread
+// and half of its columns; they also scale Q S^T, a token and half of the columns): they read V by columns and put the three parts of w v into tensor
 // memory as the A operand, 32 tokens at a time in two alternating buffers, then add the product
 // to their registers and write the bf16 copy of S for the next chunk's Q S^T.
 //
@@ -44,14 +44,16 @@ namespace {
 
 constexpr int kC = 128;                        // tokens per chunk; also dk and the value columns of a CTA
 constexpr int kThreads = 512;
-constexpr int kSlots = 5;
+// Tiles of the load ring: the state-only launch has the room of S's copy and of O's rows for one more.
+__host__ __device__ constexpr int ring_slots(bool state) { return state ? 6 : 5; }
+constexpr int kMaxSlots = 6;
 constexpr uint32_t kTile = 128 * 128 * 2, kHalf = kTile / 2;
 constexpr float kLogZero = -130.f;             // log2 of a decay of zero: 2^-130 is flushed to zero
 constexpr int kMaxSegments = 8;
 constexpr int kMaxDevices = 64;
 
 enum Bars {
-    B_F = 0, B_E = B_F + kSlots, B_GF = B_E + kSlots, B_GE = B_GF + 2, B_SF = B_GE + 2, B_PF, B_OQ, B_OF, B_OE, B_SOP,
+    B_F = 0, B_E = B_F + kMaxSlots, B_GF = B_E + kMaxSlots, B_GE = B_GF + 2, B_SF = B_GE + 2, B_PF, B_OQ, B_OF, B_OE, B_SOP,
     B_WF, B_WE = B_WF + 4, B_DF = B_WE + 4, B_DRAIN = B_DF + 2, kBars
 };
 
@@ -84,8 +86,8 @@ struct TcArgs {
     int total, batch, heads_v, heads_k, per_seq, segments;   // per_seq: 128-column items of a sequence
 };
 
-constexpr uint32_t kStage = 4 * 32 * 128;       // rows of O on their way out, half a row at a time
-constexpr uint32_t kSmem = kSlots * kTile + kTile + kStage + 2 * sizeof(Gates) + 1024;
+constexpr uint32_t kStage = 4 * 4096;          // rows of O on their way out: 32 rows of 64 columns a warp
+constexpr uint32_t kSmem = 6 * kTile + kStage + 2 * sizeof(Gates) + 1024;
 
 // Rows [valid, 128) of a tile of tokens become zero (they belong to another sequence).
 __device__ __forceinline__ void zero_rows(uint8_t *tile, int valid, int lane)
@@ -118,17 +120,18 @@ __device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0
 template <int NH, bool kState>
 __global__ void __launch_bounds__(kThreads, 1)
 linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                 const __grid_constant__ CUtensorMap tm_v, const TcArgs a)
+                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o, const TcArgs a)
 {
     constexpr int kDv = kC / NH;
     constexpr int kLoads = kState ? 2 : 3;     // tiles per chunk: K, (Q,) V
+    constexpr int kSlots = ring_slots(kState);
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ uint64_t bars[kBars];
     __shared__ volatile int aborted;
     __shared__ uint32_t tmem_s;
     uint8_t *smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
-    uint8_t *sop = smem + kSlots * kTile;      // the bf16 state, K-major
-    uint8_t *stage = sop + kTile;
+    uint8_t *sop = smem + 5 * kTile;           // the bf16 state, K-major
+    uint8_t *stage = smem + 6 * kTile;
     Gates *gates = reinterpret_cast<Gates *>(stage + kStage);
     auto bar = [&](int i) { return ptx::smem_u32(&bars[i]); };
     const uint32_t ring = ptx::smem_u32(smem), sop_u = ptx::smem_u32(sop);
@@ -160,10 +163,10 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         ptx::prefetch_tensormap(&tm_k);
         ptx::prefetch_tensormap(&tm_v);
         for (int i = 0; i < kBars; ++i) {
-            const int count = i == B_PF || i == B_OE || (i >= B_WF && i < B_WE) ? 4
-                              : i == B_SOP                                       ? 8
-                              : i == B_GE || i == B_GE + 1                       ? 12
-                                                                                 : 1;
+            const int count = i == B_OE || (i >= B_WF && i < B_WE)   ? 4
+                              : i == B_SOP                           ? 8
+                              : i == B_PF || i == B_GE || i == B_GE + 1 ? 12
+                                                                     : 1;
             ptx::mbar_init(bar(i), count);
         }
         ptx::fence_mbar_init();
@@ -177,10 +180,12 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = tmem_s;
-    // Load numbers of a chunk: K, then Q, then V.
-    auto load_k = [&](int i) { return kLoads * i; };
-    auto load_q = [&](int i) { return kLoads * i + 1; };
-    auto load_v = [&](int i) { return kLoads * i + kLoads - 1; };
+    // Load numbers of a chunk: Q, V, K.  In this order a load takes the slot of V or K of the chunk
+    // before last, or of Q of the last one, which is free first; with K first, V waited for the
+    // last chunk's update and came late.
+    auto load_q = [&](int i) { return kLoads * i; };
+    auto load_v = [&](int i) { return kLoads * i + kLoads - 2; };
+    auto load_k = [&](int i) { return kLoads * i + kLoads - 1; };
 
     // Tokens 32 s .. 32 s + 31 of chunk i as w v, for the value columns of this warp's quarter of the lanes, in
     // three parts of 16 columns from `col` on.
@@ -244,8 +249,8 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 for (; loads < kLoads * n; ++loads) {
                     const int s = loads % kSlots, i = loads / kLoads, what = loads % kLoads;
                     if (loads >= kSlots && !wait(B_E + s, (uint32_t)(loads / kSlots - 1), 1)) break;
-                    const bool is_v = what == kLoads - 1;
-                    const CUtensorMap *m = is_v ? &tm_v : what == 0 ? &tm_k : &tm_q;
+                    const bool is_v = what == kLoads - 2;
+                    const CUtensorMap *m = is_v ? &tm_v : what == kLoads - 1 ? &tm_k : &tm_q;
                     ptx::mbar_expect_tx(bar(B_F + s), kTile);
                     for (int hh = 0; hh < 2; ++hh)
                         ptx::tma_load_3d(ring + s * kTile + hh * kHalf, m, hh * 64, is_v ? item : g, seq.x + (c0 + i) * kC, bar(B_F + s));
@@ -468,7 +473,6 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 const Gates &G = gates[i & 1];
                 if (!warp_wait(B_GF + (i & 1), (uint32_t)(i >> 1), 20) || !warp_wait(B_SF, (uint32_t)i, 21)) break;
                 ptx::tc_fence_after();
-                float gamma[NH];
 #pragma unroll 1
                 for (int J = 0; J < 4; ++J) {  // 32 tokens j: read the scores, write P over them
                     uint32_t sv[32];
@@ -505,7 +509,6 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                                 pk[2 * e] = pack2(p[0], p[1]);
                                 pk[2 * e + 1] = pack2(p[2], p[3]);
                             }
-                            gamma[h] = ptx::ex2_approx((float)(quad == 0 ? 0.0 : G.all[h] - G.after[h][quad - 1]) + rel);
                         } else {
 #pragma unroll
                             for (int e = 0; e < 16; ++e) pk[e] = 0u;
@@ -515,60 +518,55 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 }
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(bar(B_GE + (i & 1)));
-                if (!warp_wait(B_OQ, (uint32_t)i, 22)) break;
-                ptx::tc_fence_after();
-                // diag(2^L) Q S^T, onto which P V is added.
-#pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t ov[32];
-                    ptx::tmem_ld32(t_o + c * 32, ov);
-                    const float gm = NH == 2 && c >= 2 ? gamma[NH - 1] : gamma[0];
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const float2 x = ptx::fmul2(make_float2(gm, gm), make_float2(__uint_as_float(ov[e]), __uint_as_float(ov[e + 1])));
-                        ov[e] = __float_as_uint(x.x);
-                        ov[e + 1] = __float_as_uint(x.y);
-                    }
-                    ptx::tmem_st32(t_o + c * 32, ov);
-                }
                 ptx::tmem_wait_st();
                 ptx::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(bar(B_PF));   // P written, Q S^T scaled
+                if (lane == 0) ptx::mbar_arrive(bar(B_PF));
+                // The output of token r, half a row at a time: by way of shared memory to global memory in
+                // one copy of the warp's 32 rows.  (16-byte stores from the lanes took five times as long, and
+                // a bulk copy for each row as long as those.)  Rows past the sequence's end are another's: the
+                // last chunk's rows are stored by their lanes.
                 if (!warp_wait(B_OF, (uint32_t)i, 23)) break;
                 ptx::tc_fence_after();
-                uint32_t out[64];              // the row in bf16: O's columns are free for the next chunk
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t ov[32];
-                    ptx::tmem_ld32(t_o + c * 32, ov);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) out[c * 16 + e] = pack2(__uint_as_float(ov[2 * e]), __uint_as_float(ov[2 * e + 1]));
-                }
-                ptx::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(bar(B_OE));
-                // To global memory by way of shared memory, half a row at a time, so that a warp's
-                // store covers whole 128-byte lines (four rows) instead of 16 bytes of 32 rows.
-                uint8_t *mine = stage + quad * 4096;
-                __nv_bfloat16 *dst = a.o + ((size_t)(seq.x + (c0 + i) * kC + quad * 32) * a.per_seq + item) * kC;
-                const int rows = len - (c0 + i) * kC - quad * 32;
-#pragma unroll
+                const int t = (c0 + i) * kC + r, t_warp = (c0 + i) * kC + quad * 32;
+#pragma unroll 1
                 for (int hh = 0; hh < 2; ++hh) {
+                    uint32_t out[32];
 #pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        *reinterpret_cast<uint4 *>(mine + lane * 128 + ((c ^ (lane & 7)) << 4)) =
-                            make_uint4(out[hh * 32 + 4 * c], out[hh * 32 + 4 * c + 1], out[hh * 32 + 4 * c + 2], out[hh * 32 + 4 * c + 3]);
-                    __syncwarp();
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t ov[32];
+                        ptx::tmem_ld32(t_o + hh * 64 + c * 32, ov);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int row = e * 4 + (lane >> 3), c = lane & 7;
-                        const uint4 x = *reinterpret_cast<const uint4 *>(mine + row * 128 + ((c ^ (row & 7)) << 4));
-                        if (row < rows) *reinterpret_cast<uint4 *>(dst + (size_t)row * a.per_seq * kC + hh * 64 + c * 8) = x;
+                        for (int e = 0; e < 16; ++e) out[c * 16 + e] = pack2(__uint_as_float(ov[2 * e]), __uint_as_float(ov[2 * e + 1]));
                     }
-                    __syncwarp();
+                    if (hh == 1) {             // O's columns are free for the next chunk
+                        ptx::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(bar(B_OE));
+                    }
+                    if (t_warp + 32 <= len) {
+                        uint8_t *mine = stage + quad * 4096;
+                        if (lane == 0) ptx::bulk_wait_read_all();   // the rows before have left
+                        __syncwarp();
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            *reinterpret_cast<uint4 *>(mine + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+                                make_uint4(out[4 * c], out[4 * c + 1], out[4 * c + 2], out[4 * c + 3]);
+                        ptx::fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            ptx::tma_store_3d(&tm_o, hh * 64, item, seq.x + t_warp, ptx::smem_u32(mine));
+                            ptx::bulk_commit();
+                        }
+                    } else if (t < len) {
+                        __nv_bfloat16 *dst = a.o + ((size_t)(seq.x + t) * a.per_seq + item) * kC + hh * 64;
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            reinterpret_cast<uint4 *>(dst)[c] = make_uint4(out[4 * c], out[4 * c + 1], out[4 * c + 2], out[4 * c + 3]);
+                    }
                 }
             }
+            if (lane == 0) ptx::bulk_wait_all();   // before the CTA's shared memory goes
         }
     } else {
         // ---------------------------------------------------------------- the state
@@ -636,6 +634,8 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 }
             }
         };
+        const uint32_t t_o = tmem + kColO + wg * 64 + lanes;
+        const int ho = NH == 2 ? wg : 0;       // head of these output columns
         bool run = true;
         float decay = 0.f;
 #pragma unroll 1
@@ -674,9 +674,31 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 if (lane == 0) ptx::mbar_arrive(bar(B_WF + wg));
             }
             if (!run) break;
-            decay = exp2f((float)gates[i & 1].all[h]);
+            const Gates &G = gates[i & 1];
+            decay = exp2f((float)G.all[h]);
+            const float gamma = ptx::ex2_approx((float)(quad == 0 ? 0.0 : G.all[ho] - G.after[ho][quad - 1]) + G.rel[ho][r]);
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar(B_GE + (i & 1)));
+            // diag(2^L) Q S^T, onto which P V is added: token r, these columns.
+            if (!(run = warp_wait(B_OQ, (uint32_t)i, 44))) break;
+            ptx::tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                uint32_t ov[16];
+                float of[16];
+                ptx::tmem_ld16(t_o + c * 16, of);
+#pragma unroll
+                for (int e = 0; e < 16; e += 2) {
+                    const float2 x = ptx::fmul2(make_float2(gamma, gamma), make_float2(of[e], of[e + 1]));
+                    ov[e] = __float_as_uint(x.x);
+                    ov[e + 1] = __float_as_uint(x.y);
+                }
+                ptx::tmem_st16(t_o + c * 16, ov);
+            }
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar(B_PF));
             if (!(run = warp_wait(B_DF + (i & 1), (uint32_t)(i >> 1), 43))) break;
             ptx::tc_fence_after();
             take(decay, kColD);
@@ -788,20 +810,20 @@ cudaError_t launch_linear_tc(const LinearArgs &l, void *workspace, size_t worksp
         a.seg_log = static_cast<double *>(workspace);
         a.seg_state = reinterpret_cast<float *>(a.seg_log + (size_t)items * a.segments * 4);
     }
-    CUtensorMap q{}, k{}, v{};
+    CUtensorMap q{}, k{}, v{}, o{};
     if (l.total > 0 && (!encode_heads(&q, l.q, l.total, l.heads_k, 1, kC) || !encode_heads(&k, l.k, l.total, l.heads_k, 1, kC) ||
-                        !encode_heads(&v, l.v, l.total, a.per_seq, 1, kC)))
+                        !encode_heads(&v, l.v, l.total, a.per_seq, 1, kC) || !encode_heads(&o, l.o, l.total, a.per_seq, 1, 32)))
         return cudaErrorInvalidValue;
     const bool one = l.dv == kC;
     if (a.segments > 1) {
         const dim3 grid((unsigned)(items * (a.segments - 1)));
-        e = one ? launch_pdl(linear_tc_kernel<1, true>, grid, kThreads, kSmem, s, q, k, v, a)
-                : launch_pdl(linear_tc_kernel<2, true>, grid, kThreads, kSmem, s, q, k, v, a);
+        e = one ? launch_pdl(linear_tc_kernel<1, true>, grid, kThreads, kSmem, s, q, k, v, o, a)
+                : launch_pdl(linear_tc_kernel<2, true>, grid, kThreads, kSmem, s, q, k, v, o, a);
         if (e != cudaSuccess) return e;
     }
     const dim3 grid((unsigned)(items * a.segments + 1));
-    return one ? launch_pdl(linear_tc_kernel<1, false>, grid, kThreads, kSmem, s, q, k, v, a)
-               : launch_pdl(linear_tc_kernel<2, false>, grid, kThreads, kSmem, s, q, k, v, a);
+    return one ? launch_pdl(linear_tc_kernel<1, false>, grid, kThreads, kSmem, s, q, k, v, o, a)
+               : launch_pdl(linear_tc_kernel<2, false>, grid, kThreads, kSmem, s, q, k, v, o, a);
 }
 
 }  // namespace stree

@@ -158,6 +158,14 @@ __device__ __forceinline__ void bulk_g2s(uint32_t dst, const void *src, uint32_t
                  : "memory");
 }
 
+// Untiled bulk copy shared -> global (both addresses 16-byte aligned, size a multiple of 16).
+__device__ __forceinline__ void bulk_s2g(void *dst, uint32_t src, uint32_t bytes)
+{
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(__cvta_generic_to_global(dst)), "r"(src),
+                 "r"(bytes)
+                 : "memory");
+}
+
 // Bulk prefetch of global memory into L2 (16-byte aligned, size a multiple of 16).
 __device__ __forceinline__ void prefetch_l2(const void *src, uint32_t bytes)
 {
