@@ -406,7 +406,8 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     double L[4], sum = 0.0;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        sum += (double)fmaxf(log2f((&al[h].x)[e]), kLogZero);
+                        const float lg = log2f((&al[h].x)[e]);
+                        sum += (double)(lg < kLogZero ? kLogZero : lg);   // a NaN stays one
                         L[e] = sum;
                     }
                     double scan = sum;

@@ -406,8 +406,9 @@ stree_status stree_tree_attention_workspace_size(int n_nodes, int batch, int ctx
  *   sequence b is row j % page_size of page page_table[b][j / page_size] (device int32
  *   [batch, max_pages]; entries past a sequence's last page are not read).  Pages are
  *   bf16 (scales NULL) or e4m3 with k_scales, v_scales uint8 [n_pages, heads_kv,
- *   page_size], the element times 2^(scale - 127) being the value.  page_size is a
- *   multiple of 8 up to 4096, n_pages * heads_kv * page_size below 2^31.  A page id
+ *   page_size], the element times 2^(scale - 127) being the value, scale in [9, 246].
+ *   page_size is a multiple of 8 up to 4096, n_pages * heads_kv * page_size below 2^31 and
+ *   max_pages * page_size up to 2^30.  A page id
  *   outside [0, n_pages), or tokens that do not fit max_pages pages, latch
  *   STREE_ERR_BAD_PAGE; no memory outside the pages is touched.
  *

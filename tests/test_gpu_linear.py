@@ -200,3 +200,57 @@ def test_steps_continue_a_prompt(st):
         st.stree_linear_step(row["q"], row["k"], row["v"], row["alpha"], row["beta"], S, step, S, skip=a["skip"])
         outs.append(step)
     _check(a, torch.cat(outs), S, "prompt and steps")
+
+
+@pytest.mark.parametrize("dv,lens", [(128, [2300, 1900]), (64, [150, 3])])
+def test_prompt_in_a_graph_and_on_another_stream(st, dv, lens):
+    """Captured with and without the split, replayed on other inputs; the same bits as an eager call."""
+    a = _inputs(lens, 2, 1, 128, dv, "bf16", seed=41)
+    o, S = torch.empty_like(a["v"]), torch.empty_like(a["S0"])
+    ws = torch.empty(max(16, st.stree_linear_prompt_workspace_size(len(lens), sum(lens), 2, 1, 128, dv)), dtype=torch.uint8,
+                     device="cuda")
+    err = torch.zeros(4, dtype=torch.int32, device="cuda")
+
+    def call():
+        st.stree_linear_prompt(a["q"], a["k"], a["v"], a["alpha"], a["beta"], a["cu"], o, S0=a["S0"], S_new=S, skip=a["skip"],
+                               err_out=err, workspace=ws)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        call()
+    torch.cuda.current_stream().wait_stream(s)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    b = _inputs(lens, 2, 1, 128, dv, "bf16", seed=42)
+    for n in ("q", "k", "v", "alpha", "beta", "S0", "skip"):
+        a[n].copy_(b[n])
+    g.replay()
+    torch.cuda.synchronize()
+    want = _run(st, b)
+    assert torch.equal(o, want[0]) and torch.equal(S, want[1]) and err.tolist() == [0, 0, 0, 0]
+
+
+@pytest.mark.parametrize("dv", [128, 64])
+def test_prompt_nan_gates_are_not_hidden(st, dv):
+    a = _inputs([200], 2, 1, 128, dv, "bf16", seed=43)
+    a["alpha"][150, 0] = float("nan")
+    o, S, _ = _run(st, a)
+    assert torch.isnan(S[0, 0]).all() and torch.isfinite(S[0, 1]).all() and torch.isfinite(o[:128]).all()
+    assert torch.isnan(o[150:, 0]).all() and torch.isfinite(o[:, 1]).all()
+
+
+def test_prompt_many_short_sequences(st):
+    """More sequences than a block has threads, most of them of one token."""
+    lens = [1] * 700 + [0, 5, 130]
+    a = _inputs(lens, 2, 1, 128, 128, "bf16", seed=44, skip=False)
+    o, S, err = _run(st, a)
+    assert err == [0, 0, 0, 0]
+    at = a["cu"].tolist()
+    pick = [0, 1, 399, 699, 700, 701, 702]
+    for b in pick:
+        lo, hi = at[b], at[b + 1]
+        one = {n: (t[lo:hi] if n in ("q", "k", "v", "alpha", "beta") else t) for n, t in a.items()}
+        one["S0"], one["cu"] = a["S0"][b:b + 1], i32([0, hi - lo])
+        _check(one, o[lo:hi], S[b:b + 1], f"of many, {b}")

@@ -344,3 +344,59 @@ def test_binding_refuses_each_tensor(st):
         st.stree_paged_attention(**{**good, "v_pages": a["v_pages"][:, :1].contiguous()})
     with pytest.raises(st.StreeError):
         st.stree_paged_attention(**{**good, "q": q[:, :7].contiguous(), "o": q[:, :7].contiguous()})
+
+
+def test_offsets_beyond_32_bits(st):
+    """Pages whose elements lie past 2^31 (and bytes past 2^32): written, attended over, read back."""
+    n_pages, hkv, page = 36000, 8, 64              # 4.7 GB of bf16 keys, and of values
+    kp = torch.empty((n_pages, hkv, page, 128), dtype=torch.bfloat16, device="cuda")
+    vp = torch.empty_like(kp)
+    table = i32([[n_pages - 1, 3, n_pages - 2], [n_pages - 3, 0, 0]])
+    rng = np.random.default_rng(11)
+    lens = [150, 40]
+    k, v = bf16(rng.normal(size=(190, hkv, 128))), bf16(rng.normal(size=(190, hkv, 128)))
+    st.stree_cache_write(k, v, i32(offsets(lens)), i32([0, 0]), table, kp, vp)
+    kc = torch.empty((2, 150, hkv, 128), dtype=torch.bfloat16, device="cuda")
+    vc = torch.empty_like(kc)
+    st.stree_cache_read(kp, vp, table, i32(lens), kc, vc)
+    torch.cuda.synchronize()
+    assert torch.equal(kc[0], k[:150]) and torch.equal(vc[1, :40], v[150:])
+    q = bf16(rng.normal(size=(2, 8, 128)))
+    o, err = _attend(st, dict(k_pages=kp, v_pages=vp, k_scales=None, v_scales=None, table=table, lens=i32(lens)), q)
+    assert err == [0, 0, 0, 0]
+    for b, (lo, hi) in enumerate(((0, 150), (150, 190))):
+        ref, oa = oracle_decode_attention(f64(q[b]), f64(k[lo:hi]), f64(v[lo:hi]), SCALE)
+        within(f64(o[b]), ref, attention_tol(ref, oa, 40.0), f"sequence {b}")
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_paged_attention_many_sequences(st, cache):
+    """More sequences than a block has threads, with empty ones among them."""
+    rng = np.random.default_rng(12)
+    lens = [int(n) for n in rng.integers(0, 20, size=700)]
+    a = _cache(rng, lens, 1, 8, cache)
+    q = bf16(rng.normal(size=(700, 4, 128)))
+    o, err = _attend(st, a, q)
+    assert err == [0, 0, 0, 0]
+    _check(a, q, o)
+
+
+def test_paged_attention_extreme_value_scales(st):
+    """Rows of zeros (the least scale) beside rows of ordinary and of very large and small scales."""
+    rng = np.random.default_rng(13)
+    lens = [3000, 300, 90]
+    a = _cache(rng, lens, 1, 16, "e4m3", stale=False)
+    vs = a["v_scales"]
+    vs.copy_(torch.from_numpy(rng.choice([100, 120, 140], size=tuple(vs.shape)).astype(np.uint8)))
+    table = a["table"].cpu().numpy()
+    for p in table[0, :100]:                       # most of the first sequence's values are zero rows
+        a["v_pages"][p].zero_()
+        vs[p] = 9
+    for p in table[2, :6]:                         # all of the third's
+        a["v_pages"][p].zero_()
+        vs[p] = 9
+    q = bf16(rng.normal(size=(3, 4, 128)))
+    o, err = _attend(st, a, q)
+    assert err == [0, 0, 0, 0]
+    _check(a, q, o)
+    assert torch.all(o[2] == 0)
