@@ -158,14 +158,6 @@ __device__ __forceinline__ void bulk_g2s(uint32_t dst, const void *src, uint32_t
                  : "memory");
 }
 
-// Untiled bulk copy shared -> global (both addresses 16-byte aligned, size a multiple of 16).
-__device__ __forceinline__ void bulk_s2g(void *dst, uint32_t src, uint32_t bytes)
-{
-    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(__cvta_generic_to_global(dst)), "r"(src),
-                 "r"(bytes)
-                 : "memory");
-}
-
 // Bulk prefetch of global memory into L2 (16-byte aligned, size a multiple of 16).
 __device__ __forceinline__ void prefetch_l2(const void *src, uint32_t bytes)
 {
@@ -208,6 +200,36 @@ __device__ __forceinline__ void prefetch_tensormap(const CUtensorMap *map)
 __device__ __forceinline__ void fence_proxy_async_smem()
 {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// ---------------------------------------------------------------- cluster launch control
+//
+// A running CTA takes over one that has not been launched yet: the request's 16-byte answer
+// arrives in shared memory and completes on the mbarrier (expect 16 bytes first).  After an
+// answer without a CTA no further request may be made.
+
+__device__ __forceinline__ void clc_request(uint32_t answer, uint32_t bar)
+{
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+                 ::"r"(answer), "r"(bar)
+                 : "memory");
+}
+
+// The CTA's blockIdx.x, or -1.
+__device__ __forceinline__ int clc_answer(uint32_t answer)
+{
+    uint32_t ok, x;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
+        "ld.shared.b128 r, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "mov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+        : "=r"(ok), "=r"(x)
+        : "r"(answer)
+        : "memory");
+    return ok ? (int)x : -1;
 }
 
 // ---------------------------------------------------------------- tcgen05
@@ -424,14 +446,6 @@ __device__ __forceinline__ void tmem_st16x8(uint32_t taddr, uint32_t r0, uint32_
                  : "memory");
 }
 
-// 32 lanes x 8 consecutive 32-bit columns stored from registers (pair with tmem_wait_st).
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
-{
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
-                 ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
-}
-
 // 32 lanes x 16 consecutive 32-bit columns stored from registers (pair with tmem_wait_st).
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16])
 {
@@ -506,13 +520,6 @@ __device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uin
         ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-
-// Moves registers between the warpgroups of a CTA (every warp of the group calls it; the
-// groups' shares add up to at most what the CTA was launched with).
-template <int kRegs>
-__device__ __forceinline__ void regs_less() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs)); }
-template <int kRegs>
-__device__ __forceinline__ void regs_more() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs)); }
 
 __device__ __forceinline__ void mbar_arrive(uint32_t bar)
 {

@@ -72,6 +72,31 @@ def test_prompt_attention_moving_maximum(st):
     _check(a, o, 520, 650, "growing scores")
 
 
+@pytest.mark.parametrize("count,longest,hq,hkv", [(300, 40, 4, 2), (129, 700, 8, 8), (515, 3, 6, 2), (5, 1300, 16, 8)])
+def test_prompt_attention_many_tiles(st, count, longest, hq, hkv):
+    # More sequences than a warp's group of them, empty ones among them, and more tiles than SMs.
+    rng = np.random.default_rng(count)
+    lens = rng.integers(0, longest + 1, count)
+    lens[0], lens[-1] = longest, 0
+    a = _inputs(lens, hq, hkv, seed=count)
+    o, err = _run(st, a)
+    assert err == [0, 0, 0, 0]
+    at = a["cu"].tolist()
+    picks = set(rng.choice(count, min(count, 12), replace=False).tolist()) | {0, count - 2, count - 1}
+    for b in sorted(picks):
+        lo, hi = at[b], at[b + 1]
+        if hi - lo > 1000:                     # of two query heads that share no keys
+            rep = hq // hkv
+            some = dict(q=a["q"][:, ::rep][:, :2], k=a["k"][:, :2], v=a["v"][:, :2])
+            _check(some, o[:, ::rep][:, :2], lo, hi, f"sequence {b}")
+        else:
+            _check(a, o, lo, hi, f"sequence {b}")
+    assert torch.isfinite(o.float()).all()
+    # The same call twice gives the same bits: which CTA takes a tile does not enter its result.
+    o2, _ = _run(st, a)
+    assert torch.equal(o, o2)
+
+
 def test_prompt_attention_keeps_to_its_sequences(st):
     a = _inputs([100, 60, 333], 4, 1, seed=4, extra=40)
     for n in ("q", "k", "v"):
