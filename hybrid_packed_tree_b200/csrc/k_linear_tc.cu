@@ -21,16 +21,17 @@
 // (24 bits), so its products are those of fp32; L is summed in 64 bits, and every exponent
 // is a difference of L's taken before it is rounded.
 //
-// Warp roles (16 warps, bounded mbarrier waits): a producer (TMA: K, Q, V tiles of 32 KB into a
-// ring of five), the MMA issuer, two gate warps (L, w and the factors of P, a chunk in turn),
+// Warp roles (16 warps, bounded mbarrier waits): a producer (TMA: Q, V, K tiles of 32 KB into a
+// ring of five), two MMA issuers (of P and O, and of the state's update, so that neither waits for
+// the other's operands), a gate warp (L, w and the factors of P; two of them in the state-only launch),
 // four warps for P and O (a token per thread; O leaves by one tensor copy a warp), and eight
 // for the state (a row of S per thread and half of its columns; they also scale Q S^T, a token
 // and half of the columns): they read V by columns and put the three parts of w v into tensor
 // memory as the A operand, 32 tokens at a time in two alternating buffers, then add the product
 // to their registers and write the bf16 copy of S for the next chunk's Q S^T.
 //
-// 8192 tokens of 32 heads of 128 x 128 (205 MB): 104 us (4802 by the walk on the CUDA cores); twelve
-// packed sequences of 4956 tokens in all, 80 heads of 64 x 128: 104 us.  Bound by the chain of a
+// 8192 tokens of 32 heads of 128 x 128 (205 MB): 97 us (4802 by the walk on the CUDA cores); twelve
+// packed sequences of 4956 tokens in all, 80 heads of 64 x 128: 85 us.  Bound by the chain of a
 // chunk's steps -- parts of w v, product, parts, product, sum, copy of S -- of about 5800
 // cycles against 3100 of the tensor cores.
 //
@@ -61,7 +62,7 @@ constexpr int kMaxDevices = 64;
 
 enum Bars {
     B_F = 0, B_E = B_F + kMaxSlots, B_GF = B_E + kMaxSlots, B_GE = B_GF + 2, B_SF = B_GE + 2, B_PF, B_OQ, B_OF, B_OE, B_SOP,
-    B_WF, B_WE = B_WF + 4, B_DF = B_WE + 4, B_DRAIN = B_DF + 2, kBars
+    B_WF, B_WE = B_WF + 4, B_DF = B_WE + 4, B_DRAIN = B_DF + 2, kBars = B_DRAIN + 2
 };
 
 // Tensor memory: Q K^T, then P over it (of every 32 columns, 16 for a head); O; the state's
@@ -172,6 +173,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         for (int i = 0; i < kBars; ++i) {
             const int count = i == B_OE || (i >= B_WF && i < B_WE)   ? 4
                               : i == B_SOP                           ? 8
+                              : i >= B_E && i < B_E + kMaxSlots && !kState ? 2
                               : i == B_PF || i == B_GE || i == B_GE + 1 ? 12
                                                                      : 1;
             ptx::mbar_init(bar(i), count);
@@ -247,6 +249,12 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         __syncwarp();
     };
 
+    auto arrived = [&](int x, int where) { return warp_wait(B_F + x % kSlots, (uint32_t)(x / kSlots), where); };
+    auto slot = [&](int x) { return ring + (x % kSlots) * kTile; };
+    auto release = [&](int x) {                // a slot that another load will use
+        if (x + kSlots < kLoads * n) ptx::mma_commit(bar(B_E + x % kSlots));
+    };
+
     int loads = 0;
     if (warp < 4) {
         if (warp == 0) {
@@ -263,112 +271,41 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         ptx::tma_load_3d(ring + s * kTile + hh * kHalf, m, hh * 64, is_v ? item : g, seq.x + (c0 + i) * kC, bar(B_F + s));
                 }
             }
-        } else if (warp == 1) {
-            // ------------------------------------------------------------ MMA issue
-            const uint32_t id_kk = ptx::idesc_bf16_kk(kC, kC), id_mn = ptx::idesc_bf16_bmn(kC, kC),
-                           id_pv = ptx::idesc_bf16_bmn(kC, kDv);
+        } else if (warp == 1 && !kState) {
+            // ------------------------------------------------------------ MMA issue: P and O
+            const uint32_t id_kk = ptx::idesc_bf16_kk(kC, kC), id_pv = ptx::idesc_bf16_bmn(kC, kDv);
             const uint64_t d_s = ptx::desc_kmajor_sw128(sop_u);
-            auto arrived = [&](int x, int where) { return warp_wait(B_F + x % kSlots, (uint32_t)(x / kSlots), where); };
-            auto slot = [&](int x) { return ring + (x % kSlots) * kTile; };
-            auto release = [&](int x) {        // a slot that another load will use
-                if (x + kSlots < kLoads * n) ptx::mma_commit(bar(B_E + x % kSlots));
-            };
-            // Tokens 64 u .. 64 u + 63 of chunk i into the state's update: 32 at a time, three parts of two
-            // steps each.
-            auto update = [&](int i, int u, uint64_t d_kt) -> bool {
-                if (!warp_wait(B_WF, (uint32_t)(2 * i + u), 14) || !warp_wait(B_WF + 1, (uint32_t)(2 * i + u), 17)) return false;
-                if (ptx::elect_one()) {
-                    ptx::tc_fence_after();
-#pragma unroll 1
-                    for (int s = 0; s < 2; ++s) {
-#pragma unroll
-                        for (int part = 0; part < 3; ++part)
-#pragma unroll
-                            for (int kk = 0; kk < 2; ++kk)
-                                ptx::mma_f16_ta(tmem + kColD, tmem + kColW + s * 64 + part * 16 + kk * 8,
-                                                ptx::desc_at(d_kt, (4 * u + 2 * s + kk) * 2048), id_mn, (u | s | part | kk) != 0);
-                        ptx::mma_commit(bar(B_WE + s));
-                    }
-                }
-                __syncwarp();
-                return true;
-            };
-            // The same of a whole chunk in the state-only launch: a buffer for each 32 tokens, and two for the
-            // update (the tokens that the state warps form come first: they have read the last but one).
-            auto update_all = [&](int i, uint64_t d_kt) -> bool {
-#pragma unroll 1
-                for (int e = 0; e < 4; ++e) {
-                    const int s = (e + 2) & 3;
-                    if (!warp_wait(B_WF + s, (uint32_t)i, 14) || (e == 0 && !warp_wait(B_WF + 3, (uint32_t)i, 17))) return false;
-                    if (ptx::elect_one()) {
-                        ptx::tc_fence_after();
-#pragma unroll
-                        for (int part = 0; part < 3; ++part)
-#pragma unroll
-                            for (int kk = 0; kk < 2; ++kk)
-                                ptx::mma_f16_ta(tmem + state_col_d(i), tmem + state_col_w(s) + part * 16 + kk * 8,
-                                                ptx::desc_at(d_kt, (2 * s + kk) * 2048), id_mn, (e | part | kk) != 0);
-                        ptx::mma_commit(bar(B_WE + s));
-                    }
-                    __syncwarp();
-                }
-                return true;
-            };
             bool ok = true;
 #pragma unroll 1
             for (int i = 0; i < n && ok; ++i) {
                 const int valid = min(kC, len - (c0 + i) * kC);
                 // The descriptors of a tile's steps are made from one per tile.
                 const uint64_t d_q = ptx::desc_kmajor_sw128(slot(load_q(i))), d_k = ptx::desc_kmajor_sw128(slot(load_k(i))),
-                               d_kt = ptx::desc_mnmajor_sw128(slot(load_k(i)), kHalf, 1024),
                                d_v = ptx::desc_mnmajor_sw128(slot(load_v(i)), kHalf, 1024);
-                if (!(ok = arrived(load_k(i), 10))) break;
-                if (valid < kC) zero_rows(smem + (load_k(i) % kSlots) * kTile, valid, lane);
-                if (!kState) {
-                    if (!(ok = arrived(load_q(i), 11))) break;
-                    if (ptx::elect_one()) {
-                        ptx::tc_fence_after();
-#pragma unroll
-                        for (int kk = 0; kk < kC / 16; ++kk)
-                            ptx::mma_f16(tmem + kColP, ptx::desc_at(d_q, (kk >> 2) * kHalf + (kk & 3) * 32),
-                                         ptx::desc_at(d_k, (kk >> 2) * kHalf + (kk & 3) * 32), id_kk, kk != 0);
-                        ptx::mma_commit(bar(B_SF));
-                    }
-                    __syncwarp();
-                }
-                // The state's update: tokens 0-63 now, the others behind Q S^T, which waits for the last
-                // chunk's O to be read.  The first product overwrites the last chunk's update, so both
-                // halves of the state warps have to have read that: they hand over w v after it.
-                if (kState) {
-                    if (!(ok = update_all(i, d_kt))) break;
-                } else if (!(ok = update(i, 0, d_kt))) {
-                    break;
-                }
-                if (!kState) {
-                    if (!(ok = warp_wait(B_SOP, (uint32_t)i, 12)) || (i > 0 && !(ok = warp_wait(B_OE, (uint32_t)(i - 1), 13)))) break;
-                    if (ptx::elect_one()) {
-                        ptx::tc_fence_after();
-#pragma unroll
-                        for (int kk = 0; kk < kC / 16; ++kk)
-                            ptx::mma_f16(tmem + kColO, ptx::desc_at(d_q, (kk >> 2) * kHalf + (kk & 3) * 32),
-                                         ptx::desc_at(d_s, (kk >> 2) * kHalf + (kk & 3) * 32), id_kk, kk != 0);
-                        ptx::mma_commit(bar(B_OQ));
-                        release(load_q(i));
-                    }
-                    __syncwarp();
-                }
-                if (!kState && !(ok = update(i, 1, d_kt))) break;
+                if (!(ok = arrived(load_q(i), 11) && arrived(load_k(i), 10))) break;
                 if (ptx::elect_one()) {
-                    ptx::mma_commit(bar(B_DF + (i & 1)));
+                    ptx::tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < kC / 16; ++kk)
+                        ptx::mma_f16(tmem + kColP, ptx::desc_at(d_q, (kk >> 2) * kHalf + (kk & 3) * 32),
+                                     ptx::desc_at(d_k, (kk >> 2) * kHalf + (kk & 3) * 32), id_kk, kk != 0);
+                    ptx::mma_commit(bar(B_SF));
                     release(load_k(i));
                 }
                 __syncwarp();
-                if (kState) {
-                    // The state warps have read V before they handed over its last part.
-                    if (ptx::elect_one()) release(load_v(i));
-                    __syncwarp();
-                    continue;
+                // Q S^T, when the last chunk's O has been read.
+                if (!(ok = warp_wait(B_SOP, (uint32_t)i, 12)) || (i > 0 && !(ok = warp_wait(B_OE, (uint32_t)(i - 1), 13)))) break;
+                if (ptx::elect_one()) {
+                    ptx::tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < kC / 16; ++kk)
+                        ptx::mma_f16(tmem + kColO, ptx::desc_at(d_q, (kk >> 2) * kHalf + (kk & 3) * 32),
+                                     ptx::desc_at(d_s, (kk >> 2) * kHalf + (kk & 3) * 32), id_kk, kk != 0);
+                    ptx::mma_commit(bar(B_OQ));
+                    release(load_q(i));
+                    release(load_q(i));        // no other reader
                 }
+                __syncwarp();
                 if (!(ok = arrived(load_v(i), 15))) break;
                 if (valid < kC) zero_rows(smem + (load_v(i) % kSlots) * kTile, valid, lane);
                 if (!(ok = warp_wait(B_PF, (uint32_t)i, 16))) break;
@@ -385,9 +322,50 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 }
                 __syncwarp();
             }
+        } else if (warp == 2) {
+            // ------------------------------------------------------------ MMA issue: the state's update
+            const uint32_t id_mn = ptx::idesc_bf16_bmn(kC, kC);
+            bool ok = true;
+#pragma unroll 1
+            for (int i = 0; i < n && ok; ++i) {
+                const int valid = min(kC, len - (c0 + i) * kC);
+                const uint64_t d_kt = ptx::desc_mnmajor_sw128(slot(load_k(i)), kHalf, 1024);
+                if (!(ok = arrived(load_k(i), 18))) break;
+                // (Q K^T may read these rows meanwhile: their scores are behind the diagonal, and not used.)
+                if (valid < kC) zero_rows(smem + (load_k(i) % kSlots) * kTile, valid, lane);
+                // 32 tokens at a time, three parts of two steps each.  The first product overwrites the last
+                // chunk's update, so both halves of the state warps have to have read that: they hand over w v
+                // after it.  The state-only launch has a buffer for each 32 tokens, and two for the update
+                // (the tokens that the state warps form come first: they have read the last but one).
+#pragma unroll 1
+                for (int e = 0; e < 4 && ok; ++e) {
+                    const int t = kState ? (e + 2) & 3 : e, s = kState ? t : e & 1;   // tokens 32 t ..; buffer
+                    const uint32_t use = kState ? (uint32_t)i : (uint32_t)(2 * i + (e >> 1));
+                    if (!(ok = warp_wait(B_WF + s, use, 14))) break;
+                    if (e == 0 && !(ok = warp_wait(B_WF + (kState ? 3 : 1), use, 17))) break;
+                    if (ptx::elect_one()) {
+                        ptx::tc_fence_after();
+                        const uint32_t col = kState ? state_col_w(s) : kColW + s * 64;
+#pragma unroll
+                        for (int part = 0; part < 3; ++part)
+#pragma unroll
+                            for (int kk = 0; kk < 2; ++kk)
+                                ptx::mma_f16_ta(tmem + (kState ? state_col_d(i) : kColD), tmem + col + part * 16 + kk * 8,
+                                                ptx::desc_at(d_kt, (2 * t + kk) * 2048), id_mn, (e | part | kk) != 0);
+                        ptx::mma_commit(bar(B_WE + s));
+                        if (e == 3) {          // the state warps have read V before they handed over its last part
+                            ptx::mma_commit(bar(B_DF + (i & 1)));
+                            release(load_k(i));
+                            release(load_v(i));
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
         } else {
             // ------------------------------------------------------------ gates
-            const int gw = warp - 2;           // warp 2 the even chunks, warp 3 the odd ones
+            constexpr int kGateWarps = kState ? 2 : 1;   // the state-only launch has a warp to spare, and less time
+            const int gw = kState ? warp >> 1 : 0;
             double total[2] = {0.0, 0.0};
             float4 al[NH], be[NH];             // of tokens 4 lane .. 4 lane + 3
             auto fetch = [&](int i) {
@@ -403,9 +381,9 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             };
             if (gw < n) fetch(gw);
 #pragma unroll 1
-            for (int i = gw; i < n; i += 2) {
-                if (i >= 2 && !warp_wait(B_GE + gw, (uint32_t)((i >> 1) - 1), 30)) break;
-                Gates &G = gates[gw];
+            for (int i = gw; i < n; i += kGateWarps) {
+                if (i >= 2 && !warp_wait(B_GE + (i & 1), (uint32_t)((i >> 1) - 1), 30)) break;
+                Gates &G = gates[i & 1];
 #pragma unroll
                 for (int h = 0; h < NH; ++h) {
                     // One scan over the lanes, four tokens each; eight lanes are a block of 32 tokens.  (Four
@@ -445,8 +423,8 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     total[h] += all;
                 }
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(bar(B_GF + gw));
-                if (i + 2 < n) fetch(i + 2);   // in flight while the other warp's chunk is worked on
+                if (lane == 0) ptx::mbar_arrive(bar(B_GF + (i & 1)));
+                if (i + kGateWarps < n) fetch(i + kGateWarps);
             }
             if (kState && lane < 2) a.seg_log[((size_t)flat * segs + seg) * 4 + gw * 2 + lane] = lane == 0 ? total[0] : total[1];
         }
@@ -574,46 +552,79 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     }
                 }
             }
-            if (lane == 0) ptx::bulk_wait_all();   // before the CTA's shared memory goes
+            if (lane == 0) ptx::bulk_wait_read_all();   // before the CTA's shared memory goes
         }
     } else {
         // ---------------------------------------------------------------- the state
         const int wg = (warp >> 2) - 2, quad = warp & 3, r = quad * 32 + lane;   // row r of S, columns 64 wg ..
         const int h = NH == 2 ? r / kDv : 0;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-        const size_t at = ((size_t)flat * kC + r) * kC + wg * 64;   // [batch, heads_v, dv] rows are flat 128-row items
         float st[64];
-        // S0, by way of the workspace when segments start from it while the last one writes S_new.
-        float *const slots = a.segments > 1 ? a.seg_state + ((size_t)flat * a.segments * kC + r) * kC + wg * 64 : nullptr;
-        const float *from = !a.S0 ? nullptr : !kState && a.segments > 1 ? slots : a.S0 + at;
-        if (kState && (seg > 0 || !a.S0)) from = nullptr;
+        // 32 rows x 64 columns of a warp, between global memory and a row per lane, by way of shared memory (the
+        // copy's room, 4 KB a warp): half of the columns at a time, an access takes four rows' 128 bytes.
+        // (Row by row a lane, each access touched 32 lines: 4.4 us to read a state and 4 to write it.)
+        uint8_t *const mine = sop + (warp - 8) * 4096;
+        const int row4 = lane >> 3, col4 = lane & 7;
+        const auto far = [&](int k) { return (size_t)((k * 4 + row4) * kC + col4 * 4); };
+        const auto near = [&](int row, int c) { return reinterpret_cast<float4 *>(mine + row * 128 + ((c ^ (row & 7)) << 4)); };
+        // st = f st + the rows at p.
+        auto fold = [&](const float *p, float f) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            float4 x = from ? reinterpret_cast<const float4 *>(from)[e] : make_float4(0.f, 0.f, 0.f, 0.f);
-            if (kState && from) {              // segment 0 copies it; its own state is taken from zero
-                reinterpret_cast<float4 *>(slots)[e] = x;
-                x = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int half = 0; half < 2; ++half) {
+                float4 x[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[k] = *reinterpret_cast<const float4 *>(p + half * 32 + far(k));
+#pragma unroll
+                for (int k = 0; k < 8; ++k) *near(k * 4 + row4, col4) = x[k];
+                __syncwarp();
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const float4 y = *near(lane, c);
+                    float *to = st + half * 32 + c * 4;
+                    to[0] = fmaf(f, to[0], y.x);
+                    to[1] = fmaf(f, to[1], y.y);
+                    to[2] = fmaf(f, to[2], y.z);
+                    to[3] = fmaf(f, to[3], y.w);
+                }
+                __syncwarp();
             }
-            st[4 * e] = x.x;
-            st[4 * e + 1] = x.y;
-            st[4 * e + 2] = x.z;
-            st[4 * e + 3] = x.w;
-        }
-        if (!kState)
+        };
+        auto store = [&](float *p) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const float *from = st + half * 32 + c * 4;
+                    *near(lane, c) = make_float4(from[0], from[1], from[2], from[3]);
+                }
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < 8; ++k) *reinterpret_cast<float4 *>(p + half * 32 + far(k)) = *near(k * 4 + row4, col4);
+                __syncwarp();
+            }
+        };
+        // S0, by way of the workspace when segments start from it while the last one writes S_new.
+        const size_t at = ((size_t)flat * kC + quad * 32) * kC + wg * 64;   // [batch, heads_v, dv] rows are flat 128-row items
+        float *const slots = a.segments > 1 ? a.seg_state + ((size_t)flat * a.segments * kC + quad * 32) * kC + wg * 64 : nullptr;
+#pragma unroll
+        for (int e = 0; e < 64; ++e) st[e] = 0.f;
+        if (kState) {
+            if (seg == 0 && a.S0)              // its own state is taken from zero
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        *reinterpret_cast<float4 *>(slots + half * 32 + far(k)) =
+                            *reinterpret_cast<const float4 *>(a.S0 + at + half * 32 + far(k));
+        } else {
+            if (a.S0) fold(a.segments > 1 ? slots : a.S0 + at, 0.f);
 #pragma unroll 1
             for (int s = 0; s < seg; ++s) {    // the segments before this one
                 const size_t p = (size_t)flat * (a.segments - 1) + s;
-                const float f = exp2f((float)(a.seg_log[p * 4 + h] + a.seg_log[p * 4 + 2 + h]));
-                const float4 *src = reinterpret_cast<const float4 *>(slots + (size_t)(s + 1) * kC * kC);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const float4 x = src[e];
-                    st[4 * e] = fmaf(f, st[4 * e], x.x);
-                    st[4 * e + 1] = fmaf(f, st[4 * e + 1], x.y);
-                    st[4 * e + 2] = fmaf(f, st[4 * e + 2], x.z);
-                    st[4 * e + 3] = fmaf(f, st[4 * e + 3], x.w);
-                }
+                fold(slots + (size_t)(s + 1) * kC * kC, exp2f((float)(a.seg_log[p * 4 + h] + a.seg_log[p * 4 + 2 + h])));
             }
+            asm volatile("bar.sync 1, 256;" ::: "memory");   // the copy's room is free
+        }
         // The bf16 copy that the next Q S^T reads: row r of this half.
         auto copy_out = [&] {
             uint8_t *dst = sop + wg * kHalf + r * 128;
@@ -713,17 +724,14 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         }
         float *dst = kState ? slots + (size_t)(seg + 1) * kC * kC
                             : last && a.S_new ? a.S_new + at : nullptr;
-        if (dst && run)
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-                reinterpret_cast<float4 *>(dst)[e] = make_float4(st[4 * e], st[4 * e + 1], st[4 * e + 2], st[4 * e + 3]);
+        if (dst && run) store(dst);        // the last Q S^T has read its copy
     }
 
     // -------------------------------------------------------------------- teardown
-    if (tid == 64 && aborted && a.err) latch_error(a.err, STREE_ERR_TIMEOUT, b, aborted, 0);
-    if (warp == 1 && aborted && ptx::elect_one()) {
-        ptx::mma_commit(bar(B_DRAIN));         // every issued MMA completes first
-        ptx::mbar_wait(bar(B_DRAIN), 0);
+    if (tid == 96 && aborted && a.err) latch_error(a.err, STREE_ERR_TIMEOUT, b, aborted, 0);
+    if ((warp == 1 || warp == 2) && aborted && ptx::elect_one()) {
+        ptx::mma_commit(bar(B_DRAIN + warp - 1));   // every issued MMA completes first
+        ptx::mbar_wait(bar(B_DRAIN + warp - 1), 0);
     }
     if (warp == 0 && aborted && loads > 0)
 #pragma unroll 1
