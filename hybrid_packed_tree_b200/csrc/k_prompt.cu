@@ -361,6 +361,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         const int r = quad * 32 + lane;        // query row = tensor-memory lane
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         const uint32_t t_s = tmem + half * kKB + lanes, t_o = tmem + 256 + half * kD + lanes;
+        const bool wide = (reinterpret_cast<uintptr_t>(a.o) & 31) == 0;   // 32-byte stores
         int done = 0, uses = 0;                // key blocks and tiles of this half before this tile
         bool run = true;
 #pragma unroll 1
@@ -448,15 +449,20 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                 const float inv = 1.f / l;     // the row's own token is never masked: l > 0
                 __nv_bfloat16 *row = a.o + ((size_t)(t.row + token) * a.heads_q + t.g * a.group + r % a.group) * kD;
 #pragma unroll
-                for (int c = 0; c < kD / 8; ++c) {
-                    uint32_t w[4];
+                for (int c = 0; c < kD / 16; ++c) {
+                    uint32_t w[8];
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(ov[8 * c + 2 * u]) * inv,
-                                                                       __uint_as_float(ov[8 * c + 2 * u + 1]) * inv);
+                    for (int u = 0; u < 8; ++u) {
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(ov[16 * c + 2 * u]) * inv,
+                                                                       __uint_as_float(ov[16 * c + 2 * u + 1]) * inv);
                         w[u] = *reinterpret_cast<const uint32_t *>(&h);
                     }
-                    *reinterpret_cast<uint4 *>(row + 8 * c) = make_uint4(w[0], w[1], w[2], w[3]);
+                    if (wide) {                // half the accesses: 490 -> 482 us on 8192 tokens, 73 -> 69 packed
+                        ptx::st_global_32b(row + 16 * c, w);
+                    } else {
+                        *reinterpret_cast<uint4 *>(row + 16 * c) = make_uint4(w[0], w[1], w[2], w[3]);
+                        *reinterpret_cast<uint4 *>(row + 16 * c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                    }
                 }
             }
             done += nh;

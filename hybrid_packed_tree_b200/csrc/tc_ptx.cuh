@@ -49,6 +49,20 @@ __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes)
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 
+// Whether a phase is complete, without waiting.
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // The thread may be suspended in the instruction (for a time the hardware
 // chooses) until the phase completes, so a waiting warp does not take issue slots
 // from working ones.  (An explicit suspend-time hint measured slower: waking
@@ -415,6 +429,14 @@ __device__ __forceinline__ void tmem_ld128(uint32_t taddr, uint32_t (&r)[128])
 }
 
 // 2^x by the hardware approximation (ex2.approx.ftz.f32; -inf gives +0).
+// 32 bytes to a 32-byte boundary.
+__device__ __forceinline__ void st_global_32b(void *p, const uint32_t *w)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
 __device__ __forceinline__ float ex2_approx(float x)
 {
     float y;

@@ -149,3 +149,16 @@ def test_prompt_attention_in_a_graph_and_on_another_stream(st):
     assert not torch.equal(o, want)
     _check(a, o, 0, 200, "replayed")
     _check(a, o, 200, 261, "replayed")
+
+
+def test_prompt_attention_output_at_a_16_byte_boundary(st):
+    a = _inputs([140, 33], 8, 2, seed=10)
+    n = a["q"].numel()
+    room = torch.full((n + 16,), 7.0, dtype=torch.bfloat16, device="cuda")
+    o = room[8:8 + n].view(a["q"].shape)
+    assert o.data_ptr() % 32 == 16
+    st.stree_prompt_attention(a["q"], a["k"], a["v"], a["cu"], o, SCALE)
+    torch.cuda.synchronize()
+    _check(a, o, 0, 140, "first sequence")
+    _check(a, o, 140, 173, "second sequence")
+    assert torch.all(room[:8] == 7.0) and torch.all(room[-8:] == 7.0)
