@@ -1,8 +1,9 @@
-"""Build ``libstree.so`` (the C ABI of include/stree.h) in-tree with nvcc for sm_100a.
+"""Build ``libstree.so`` (the C ABI of include/stree.h) in-tree with nvcc for sm_100a, and
+``_bind.so`` (the binding's argument check, csrc/bind.cpp) with g++.
 
     python -m hybrid_packed_tree_b200.build [--force] [--verbose]
 
-The library is written next to this file so that it travels with the source
+Both are written next to this file so that they travel with the source
 tree; nothing is installed into site-packages.
 """
 from __future__ import annotations
@@ -12,12 +13,15 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libstree.so")
+BIND = os.path.join(PKG, "_bind.so")
+BIND_SRC = os.path.join(CSRC, "bind.cpp")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -36,8 +40,25 @@ def is_stale() -> bool:
     return any(os.path.getmtime(p) > t for p in _deps())
 
 
+def build_bind(force: bool = False) -> str:
+    """Compile csrc/bind.cpp against the installed torch into _bind.so; returns its path."""
+    if not force and os.path.exists(BIND) and os.path.getmtime(BIND) >= os.path.getmtime(BIND_SRC):
+        return BIND
+    import torch
+    at = os.path.dirname(torch.__file__)
+    tmp = BIND + f".tmp{os.getpid()}"
+    subprocess.run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+                    f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+                    "-I", sysconfig.get_paths()["include"], "-I", os.path.join(at, "include"),
+                    "-I", os.path.join(at, "include", "torch", "csrc", "api", "include"), "-o", tmp, BIND_SRC,
+                    "-L", os.path.join(at, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10"], check=True)
+    os.replace(tmp, BIND)
+    return BIND
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile every .cu under csrc/ into libstree.so; returns its path."""
+    """Compile every .cu under csrc/ into libstree.so, and _bind.so; returns the library's path."""
+    build_bind(force)
     if not force and not is_stale():
         return LIB
     nvcc = os.environ.get("NVCC", "nvcc")
