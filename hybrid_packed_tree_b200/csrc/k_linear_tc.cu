@@ -27,11 +27,11 @@
 // four warps for P and O (a token per thread; O leaves by one tensor copy a warp), and eight
 // for the state (a row of S per thread and half of its columns; they also scale Q S^T, a token
 // and half of the columns): they read V by columns and put the three parts of w v into tensor
-// memory as the A operand, 32 tokens at a time in two alternating buffers, then add the product
+// memory as the A operand, 16 tokens at a time in two alternating buffers for each half, then add the product
 // to their registers and write the bf16 copy of S for the next chunk's Q S^T.
 //
-// 8192 tokens of 32 heads of 128 x 128 (205 MB): 97 us (4802 by the walk on the CUDA cores); twelve
-// packed sequences of 4956 tokens in all, 80 heads of 64 x 128: 85 us.  Bound by the chain of a
+// 8192 tokens of 32 heads of 128 x 128 (205 MB): 96 us (4802 by the walk on the CUDA cores); twelve
+// packed sequences of 4956 tokens in all, 80 heads of 64 x 128: 84 us.  Bound by the chain of a
 // chunk's steps -- parts of w v, product, parts, product, sum, copy of S -- of about 5800
 // cycles against 3100 of the tensor cores.
 //
@@ -79,7 +79,7 @@ struct Gates {                                 // of one chunk, per head
     float beta[2][kC];
     float fac[2][kC];                          // 2^(L at the end of j's block - L_j) beta_j
     float w[2][kC];
-    double after[2][4];                        // log decay from the end of each 32-token block to the chunk's
+    float step[2][4][4];                       // of block i: log decay from the end of block J < i to its start, and [3] from the chunk's
     double all[2];                             // of the whole chunk
 };
 
@@ -166,6 +166,10 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 
     auto wait = [&](int i, uint32_t parity, int where) { return wait_one(&aborted, bar(i), parity, where); };
     auto warp_wait = [&](int i, uint32_t parity, int where) { return wait_warp(&aborted, bar(i), parity, where); };
+    auto both_wait = [&](int i, uint32_t i_parity, int j, uint32_t j_parity, int where) {
+        const bool ok = wait_one(&aborted, bar(i), i_parity, where) && wait_one(&aborted, bar(j), j_parity, where + 1);
+        return __all_sync(0xffffffffu, ok) != 0;
+    };
     if (tid == 0) {
         ptx::prefetch_tensormap(&tm_q);
         ptx::prefetch_tensormap(&tm_k);
@@ -196,9 +200,9 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     auto load_v = [&](int i) { return kLoads * i + kLoads - 2; };
     auto load_k = [&](int i) { return kLoads * i + kLoads - 1; };
 
-    // Tokens 32 s .. 32 s + 31 of chunk i as w v, for the value columns of this warp's quarter of the lanes, in
-    // three parts of 16 columns from `col` on.
-    auto form = [&](int i, int s, uint32_t col) {
+    // Tokens t0 .. t0 + 15 of chunk i as w v, for the value columns of this warp's quarter of the lanes, in
+    // three parts of 8 columns, `stride` apart, from `col` on.
+    auto form = [&](int i, int t0, uint32_t col, uint32_t stride) {
         const Gates &G = gates[i & 1];
         const int x = load_v(i), valid = min(kC, len - (c0 + i) * kC), quad = warp & 3;
         const int h = NH == 2 ? quad >> 1 : 0;
@@ -206,44 +210,44 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const uint32_t v = ring + (x % kSlots) * kTile + (quad >> 1) * kHalf + (lane & 7) * 128 +
                            ((((quad & 1) * 4 + (lane >> 3)) ^ (lane & 7)) << 4);
         const uint32_t t_w = tmem + col + ((uint32_t)(quad * 32) << 16);
-#pragma unroll 1
-        for (int z = 0; z < 2; ++z) {  // 16 tokens
-            // Transposed 8 x 8 tiles: a register is two tokens (2 (lane % 4), + 1) of column lane / 4.
-            const int t0 = s * 32 + z * 16, t = t0 + (lane & 3) * 2;
-            uint32_t raw[2][4];
-            ldsm4_t(v + t0 * 128, raw[0]);
-            ldsm4_t(v + t0 * 128 + 1024, raw[1]);
-            const float2 w[2] = {*reinterpret_cast<const float2 *>(&G.w[h][t]), *reinterpret_cast<const float2 *>(&G.w[h][t + 8])};
-            float2 y[2][4];
+        // Transposed 8 x 8 tiles: a register is two tokens (2 (lane % 4), + 1) of column lane / 4.
+        const int t = t0 + (lane & 3) * 2;
+        uint32_t raw[2][4];
+        ldsm4_t(v + t0 * 128, raw[0]);
+        ldsm4_t(v + t0 * 128 + 1024, raw[1]);
+        const float2 w[2] = {*reinterpret_cast<const float2 *>(&G.w[h][t]), *reinterpret_cast<const float2 *>(&G.w[h][t + 8])};
+        float2 y[2][4];
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) y[e][c] = ptx::fmul2(w[e], make_float2(low(raw[e][c]), high(raw[e][c])));
+        if (t0 + 16 > valid)       // another sequence's rows
 #pragma unroll
             for (int e = 0; e < 2; ++e)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) y[e][c] = ptx::fmul2(w[e], make_float2(low(raw[e][c]), high(raw[e][c])));
-            if (t0 + 16 > valid)       // another sequence's rows
+                for (int c = 0; c < 4; ++c) {
+                    y[e][c].x = t + 8 * e < valid ? y[e][c].x : 0.f;
+                    y[e][c].y = t + 8 * e + 1 < valid ? y[e][c].y : 0.f;
+                }
+        // Three parts of eight bits each, cut off rather than rounded: their sum is exact.
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
+        for (int part = 0; part < 3; ++part) {
+            uint32_t p[2][4];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        y[e][c].x = t + 8 * e < valid ? y[e][c].x : 0.f;
-                        y[e][c].y = t + 8 * e + 1 < valid ? y[e][c].y : 0.f;
-                    }
-            // Three parts of eight bits each, cut off rather than rounded: their sum is exact.
+            for (int e = 0; e < 2; ++e)
 #pragma unroll
-            for (int part = 0; part < 3; ++part) {
-                uint32_t p[2][4];
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const uint32_t bx = __float_as_uint(y[e][c].x), by = __float_as_uint(y[e][c].y);
-                        p[e][c] = __byte_perm(bx, by, 0x7632);
-                        if (part < 2)
-                            y[e][c] = ptx::ffma2(make_float2(low(p[e][c]), high(p[e][c])), make_float2(-1.f, -1.f), y[e][c]);
-                    }
-                ptx::tmem_st16x8(t_w + part * 16 + z * 8, p[0][0], p[0][1], p[1][0], p[1][1]);
-                ptx::tmem_st16x8(t_w + (16u << 16) + part * 16 + z * 8, p[0][2], p[0][3], p[1][2], p[1][3]);
-            }
+                for (int c = 0; c < 4; ++c) {
+                    const uint32_t bx = __float_as_uint(y[e][c].x), by = __float_as_uint(y[e][c].y);
+                    p[e][c] = __byte_perm(bx, by, 0x7632);
+                    if (part < 2)
+                        y[e][c] = ptx::ffma2(make_float2(low(p[e][c]), high(p[e][c])), make_float2(-1.f, -1.f), y[e][c]);
+                }
+            ptx::tmem_st16x8(t_w + part * stride, p[0][0], p[0][1], p[1][0], p[1][1]);
+            ptx::tmem_st16x8(t_w + (16u << 16) + part * stride, p[0][2], p[0][3], p[1][2], p[1][3]);
         }
+    };
+    // The parts are there: to be followed by one arrival a warp.
+    auto formed = [&] {
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         __syncwarp();
@@ -333,27 +337,30 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 if (!(ok = arrived(load_k(i), 18))) break;
                 // (Q K^T may read these rows meanwhile: their scores are behind the diagonal, and not used.)
                 if (valid < kC) zero_rows(smem + (load_k(i) % kSlots) * kTile, valid, lane);
-                // 32 tokens at a time, three parts of two steps each.  The first product overwrites the last
-                // chunk's update, so both halves of the state warps have to have read that: they hand over w v
-                // after it.  The state-only launch has a buffer for each 32 tokens, and two for the update
-                // (the tokens that the state warps form come first: they have read the last but one).
+                // Three parts each.  The first product overwrites the last chunk's update, so both halves of the
+                // state warps have to have read that: they hand over w v after it.  16 tokens at a time, two
+                // buffers for each half, so that one is formed while the other is multiplied.  The state-only
+                // launch has a buffer for each 32 tokens, and two for the update (the tokens that the state
+                // warps form come first: they have read the last but one).
+                constexpr int kSteps = kState ? 4 : 8, kInner = kState ? 2 : 1;
 #pragma unroll 1
-                for (int e = 0; e < 4 && ok; ++e) {
-                    const int t = kState ? (e + 2) & 3 : e, s = kState ? t : e & 1;   // tokens 32 t ..; buffer
-                    const uint32_t use = kState ? (uint32_t)i : (uint32_t)(2 * i + (e >> 1));
+                for (int e = 0; e < kSteps && ok; ++e) {
+                    const int t = kState ? (e + 2) & 3 : e;               // tokens 32 t .. or 16 t ..
+                    const int s = kState ? t : 2 * (e & 1) + (e >> 1 & 1);   // the buffer
+                    const uint32_t use = kState ? (uint32_t)i : (uint32_t)(2 * i + (e >> 2));
                     if (!(ok = warp_wait(B_WF + s, use, 14))) break;
-                    if (e == 0 && !(ok = warp_wait(B_WF + (kState ? 3 : 1), use, 17))) break;
+                    if (e == 0 && !(ok = warp_wait(B_WF + (kState ? 3 : 2), use, 17))) break;
                     if (ptx::elect_one()) {
                         ptx::tc_fence_after();
-                        const uint32_t col = kState ? state_col_w(s) : kColW + s * 64;
+                        const uint32_t col = kState ? state_col_w(s) : kColW + s * 32;
 #pragma unroll
                         for (int part = 0; part < 3; ++part)
 #pragma unroll
-                            for (int kk = 0; kk < 2; ++kk)
-                                ptx::mma_f16_ta(tmem + (kState ? state_col_d(i) : kColD), tmem + col + part * 16 + kk * 8,
-                                                ptx::desc_at(d_kt, (2 * t + kk) * 2048), id_mn, (e | part | kk) != 0);
+                            for (int kk = 0; kk < kInner; ++kk)
+                                ptx::mma_f16_ta(tmem + (kState ? state_col_d(i) : kColD), tmem + col + part * 8 * kInner + kk * 8,
+                                                ptx::desc_at(d_kt, (kInner * t + kk) * 2048), id_mn, (e | part | kk) != 0);
                         ptx::mma_commit(bar(B_WE + s));
-                        if (e == 3) {          // the state warps have read V before they handed over its last part
+                        if (e == kSteps - 1) { // the state warps have read V before they handed over its last part
                             ptx::mma_commit(bar(B_DF + (i & 1)));
                             release(load_k(i));
                             release(load_v(i));
@@ -405,7 +412,9 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     const double end = __shfl_sync(0xffffffffu, scan, lane | 7);
                     const double prev = __shfl_sync(0xffffffffu, scan, max((lane & 24) - 1, 0));
                     const double start = lane < 8 ? 0.0 : prev;
-                    if ((lane & 7) == 7) G.after[h][lane >> 3] = all - scan;
+                    const int quad = lane >> 2 & 3, J = lane & 3;
+                    const double to = __shfl_sync(0xffffffffu, scan, max(8 * quad - 1, 0)), from = __shfl_sync(0xffffffffu, scan, 8 * J + 7);
+                    if (lane < 16) G.step[h][quad][J] = (float)((quad ? to : 0.0) - (J == 3 ? 0.0 : from));
                     float4 rel, fac, w;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -441,7 +450,9 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 for (int s = 0; s < 2; ++s) {
                     if (i > 0 && !(ok = warp_wait(B_WE + s, (uint32_t)(i - 1), 52))) break;
                     ptx::tc_fence_after();
-                    form(i, s, state_col_w(s));
+#pragma unroll 1
+                    for (int z = 0; z < 2; ++z) form(i, s * 32 + z * 16, state_col_w(s) + z * 8, 16);
+                    formed();
                     if (lane == 0) ptx::mbar_arrive(bar(B_WF + s));
                 }
                 if (!ok) break;
@@ -457,7 +468,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 #pragma unroll 1
             for (int i = 0; i < n; ++i) {
                 const Gates &G = gates[i & 1];
-                if (!warp_wait(B_GF + (i & 1), (uint32_t)(i >> 1), 20) || !warp_wait(B_SF, (uint32_t)i, 21)) break;
+                if (!both_wait(B_GF + (i & 1), (uint32_t)(i >> 1), B_SF, (uint32_t)i, 20)) break;
                 ptx::tc_fence_after();
 #pragma unroll 1
                 for (int J = 0; J < 4; ++J) {  // 32 tokens j: read the scores, write P over them
@@ -470,7 +481,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         const float rel = G.rel[h][r];
                         if (J < quad) {
                             // L_i less L at the end of block J.
-                            const float row = ptx::ex2_approx((float)(G.after[h][J] - G.after[h][quad - 1]) + rel);
+                            const float row = ptx::ex2_approx(G.step[h][quad][J] + rel);
                             const float2 row2 = make_float2(row, row);
 #pragma unroll
                             for (int e = 0; e < 8; ++e) {
@@ -668,7 +679,9 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                                 (i == 0 || warp_wait(B_WE + 2 + wg, (uint32_t)(i - 1), 42))))
                         break;
                     ptx::tc_fence_after();
-                    form(i, 2 + wg, state_col_w(2 + wg));
+#pragma unroll 1
+                    for (int z = 0; z < 2; ++z) form(i, (2 + wg) * 32 + z * 16, state_col_w(2 + wg) + z * 8, 16);
+                    formed();
                     if (lane == 0) ptx::mbar_arrive(bar(B_WF + 2 + wg));
                     next = exp2f((float)gates[i & 1].all[h]);
                     __syncwarp();
@@ -683,19 +696,20 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 continue;
             }
             copy_out();                        // Q S^T of the last chunk was issued before its update was done
-            if (!(run = warp_wait(B_GF + (i & 1), (uint32_t)(i >> 1), 40) && warp_wait(B_F + x % kSlots, (uint32_t)(x / kSlots), 41))) break;
+            if (!(run = both_wait(B_GF + (i & 1), (uint32_t)(i >> 1), B_F + x % kSlots, (uint32_t)(x / kSlots), 40))) break;
 #pragma unroll 1
-            for (int u = 0; u < 2; ++u) {
-                const int s = 2 * u + wg, uses = 2 * i + u;
-                if (uses > 0 && !(run = warp_wait(B_WE + wg, (uint32_t)(uses - 1), 42))) break;
+            for (int j = 0; j < 4; ++j) {
+                const int mine = 2 * wg + (j & 1), uses = 2 * i + (j >> 1);
+                if (uses > 0 && !(run = warp_wait(B_WE + mine, (uint32_t)(uses - 1), 42))) break;
                 ptx::tc_fence_after();
-                form(i, s, kColW + wg * 64);
-                if (lane == 0) ptx::mbar_arrive(bar(B_WF + wg));
+                form(i, (2 * j + wg) * 16, kColW + mine * 32, 8);
+                formed();
+                if (lane == 0) ptx::mbar_arrive(bar(B_WF + mine));
             }
             if (!run) break;
             const Gates &G = gates[i & 1];
             decay = exp2f((float)G.all[h]);
-            const float gamma = ptx::ex2_approx((float)(quad == 0 ? 0.0 : G.all[ho] - G.after[ho][quad - 1]) + G.rel[ho][r]);
+            const float gamma = ptx::ex2_approx(G.step[ho][quad][3] + G.rel[ho][r]);
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar(B_GE + (i & 1)));
             // diag(2^L) Q S^T, onto which P V is added: token r, these columns.
