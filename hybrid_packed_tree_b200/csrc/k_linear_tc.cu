@@ -31,9 +31,10 @@
 // to their registers and write the bf16 copy of S for the next chunk's Q S^T.
 //
 // 8192 tokens of 32 heads of 128 x 128 (205 MB): 96 us (4802 by the walk on the CUDA cores); twelve
-// packed sequences of 4956 tokens in all, 80 heads of 64 x 128: 84 us.  Bound by the chain of a
-// chunk's steps -- parts of w v, product, parts, product, sum, copy of S -- of about 5800
-// cycles against 3100 of the tensor cores.
+// packed sequences of 4956 tokens in all, 80 heads of 64 x 128: 84 us.  A chunk takes 5750
+// cycles, against 3100 of the tensor cores and 3800 of shared memory (operands, copies, rows of O):
+// the loop that bounds it runs over the warps of P and O (O's rows read and sent out 1500, P 2000 for
+// the first tokens and 2800 for the last, P V 800, Q K^T of the next chunk between).
 //
 // P below the diagonal 32 x 32 blocks is a product of a row factor 2^(L_i - L_J) and a column
 // factor 2^(L_J - L_j) beta_j, J the last token of j's block: both at most 1, and one exponential per

@@ -503,7 +503,8 @@ stree_status stree_paged_attention_workspace_size(int heads_q, int heads_kv, int
  * its largest finite magnitude to 448 or below (scale within [9, 246]), and its values are
  * rounded to the nearest e4m3 (ties to even; infinities become the largest, NaN stays).
  * A sequence whose tokens do not fit is not written at all; a token whose page is out of
- * range is not written.  Sequences that write must not share the pages that they write
+ * range is not written.  Beside offsets that are not ascending (STREE_ERR_BAD_SEQ) tokens of
+ * other sequences may be left unwritten too.  Sequences that write must not share the pages that they write
  * (no order is kept between two writes of one position).
  */
 stree_status stree_cache_write(const void *k, const void *v, const int32_t *cu_seqlens, const int32_t *start,
