@@ -11,10 +11,10 @@
 //
 // A CTA walks the chunks of one sequence and 128 value columns (one head of 128, or two of 64 that
 // share keys and queries: their Q K^T is one product).  Few sequences of many tokens are
-// cut into segments: a first launch takes every segment but the last from a zero state and
-// leaves its state and log decay in the workspace, and the walk of a segment starts from S0
-// folded with its predecessors' (the recurrence is linear).  The first launch also copies S0,
-// which the last segment may overwrite while others start from it.
+// cut into segments.  Three launches: the states and log decays of the middle segments from a zero
+// state, left in the workspace; beside them, on other SMs, the whole walk of the first, a shorter
+// one; and the walks of the others, each from the first one's state folded with those between (the
+// recurrence is linear).
 //
 // Precision.  P and the copy of S that Q multiplies are rounded to bf16 (they only enter o,
 // itself bf16).  The state is kept in fp32 registers and receives w_j v_j as three bf16 parts
@@ -30,7 +30,7 @@
 // memory as the A operand, 16 tokens at a time in two alternating buffers for each half, then add the product
 // to their registers and write the bf16 copy of S for the next chunk's Q S^T.
 //
-// 8192 tokens of 32 heads of 128 x 128 (205 MB): 96 us (4802 by the walk on the CUDA cores); twelve
+// 8192 tokens of 32 heads of 128 x 128 (205 MB): 92 us (4802 by the walk on the CUDA cores); twelve
 // packed sequences of 4956 tokens in all, 80 heads of 64 x 128: 84 us.  A chunk takes 5750
 // cycles, against 3100 of the tensor cores and 3800 of shared memory (operands, copies, rows of O):
 // the loop that bounds it runs over the warps of P and O (O's rows read and sent out 1500, P 2000 for
@@ -58,7 +58,9 @@ __host__ __device__ constexpr int ring_slots(bool state) { return state ? 6 : 5;
 constexpr int kMaxSlots = 6;
 constexpr uint32_t kTile = 128 * 128 * 2, kHalf = kTile / 2;
 constexpr float kLogZero = -130.f;             // log2 of a decay of zero: 2^-130 is flushed to zero
-constexpr int kMaxSegments = 8;
+constexpr int kMaxSegments = 9;
+// Length of the first segment to the others': a chunk of the whole walk takes 4.3 us, of the state alone 2.4.
+constexpr int kFirstWeight = 9, kOtherWeight = 16;
 constexpr int kMaxDevices = 64;
 
 enum Bars {
@@ -89,10 +91,11 @@ struct TcArgs {
     const int32_t *cu;
     __nv_bfloat16 *o;
     float *S_new;
-    float *seg_state;                          // [item][segments][128][128]: S0, then every segment's but the last
-    double *seg_log;                           // [item][segments - 1][even, odd chunks][2]
+    float *seg_state;                          // [item][segments - 1][128][128]: of every segment but the last
+    double *seg_log;                           // [item][segments - 1][even, odd chunks][2]: the first's is not used
     int32_t *err;
     int total, batch, heads_v, heads_k, per_seq, segments;   // per_seq: 128-column items of a sequence
+    int seg_first, seg_count;                  // of this launch
 };
 
 constexpr uint32_t kStage = 4 * 4096;          // rows of O on their way out: 32 rows of 64 columns a warp
@@ -146,24 +149,31 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const uint32_t ring = ptx::smem_u32(smem), sop_u = ptx::smem_u32(sop);
     const int tid = threadIdx.x, lane = tid & 31, warp = ptx::warp_index();
 
-    pdl_start();
-    if (!kState && blockIdx.x == gridDim.x - 1) {   // the error word
+    // The first segment's launch runs beside the state-only one, which lets it start once the kernels
+    // before are done, and waits for that one's end at its own.
+    const bool beside = !kState && a.segments > 1 && a.seg_first == 0;
+    if (!beside) wait_dependency();
+    launch_dependents();
+    if (!kState && a.seg_first == 0 && blockIdx.x == gridDim.x - 1) {   // the error word
         PageCheck c{};
         c.cu = a.cu;
         c.batch = a.batch;
         c.total = a.total;
         check_pages(c, a.err);
+        if (beside) wait_dependency();
         return;
     }
-    const int segs = kState ? a.segments - 1 : a.segments;
-    const int seg = blockIdx.x % segs, flat = blockIdx.x / segs;   // flat: (sequence, 128-column item)
+    const int seg = a.seg_first + blockIdx.x % a.seg_count, flat = blockIdx.x / a.seg_count;   // flat: (sequence, 128-column item)
     const int item = flat % a.per_seq, b = flat / a.per_seq;
     const int head0 = item * NH, g = head0 / (a.heads_v / a.heads_k);
     const int2 seq = seq_range(a.cu, b, a.total);
     const int len = seq.y - seq.x, chunks = (len + kC - 1) / kC;
-    const int c0 = (int)((long long)chunks * seg / a.segments), n = (int)((long long)chunks * (seg + 1) / a.segments) - c0;
+    const auto begin = [&](int s) {
+        return s == 0 ? 0 : (int)((long long)chunks * (kFirstWeight + kOtherWeight * (s - 1)) / (kFirstWeight + kOtherWeight * (a.segments - 1)));
+    };
+    const int c0 = begin(seg), n = begin(seg + 1) - c0;
     const bool last = seg == a.segments - 1;
-    if (n == 0 && !kState && !last) return;    // nothing to put out
+    if (n == 0 && !kState && seg > 0 && !last) return;   // nothing to put out
 
     auto wait = [&](int i, uint32_t parity, int where) { return wait_one(&aborted, bar(i), parity, where); };
     auto warp_wait = [&](int i, uint32_t parity, int where) { return wait_warp(&aborted, bar(i), parity, where); };
@@ -436,7 +446,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 if (lane == 0) ptx::mbar_arrive(bar(B_GF + (i & 1)));
                 if (i + kGateWarps < n) fetch(i + kGateWarps);
             }
-            if (kState && lane < 2) a.seg_log[((size_t)flat * segs + seg) * 4 + gw * 2 + lane] = lane == 0 ? total[0] : total[1];
+            if (kState && lane < 2) a.seg_log[((size_t)flat * (a.segments - 1) + seg) * 4 + gw * 2 + lane] = lane == 0 ? total[0] : total[1];
         }
     } else if (warp < 8) {
         // ---------------------------------------------------------------- P and O
@@ -579,28 +589,6 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const int row4 = lane >> 3, col4 = lane & 7;
         const auto far = [&](int k) { return (size_t)((k * 4 + row4) * kC + col4 * 4); };
         const auto near = [&](int row, int c) { return reinterpret_cast<float4 *>(mine + row * 128 + ((c ^ (row & 7)) << 4)); };
-        // st = f st + the rows at p.
-        auto fold = [&](const float *p, float f) {
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                float4 x[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) x[k] = *reinterpret_cast<const float4 *>(p + half * 32 + far(k));
-#pragma unroll
-                for (int k = 0; k < 8; ++k) *near(k * 4 + row4, col4) = x[k];
-                __syncwarp();
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const float4 y = *near(lane, c);
-                    float *to = st + half * 32 + c * 4;
-                    to[0] = fmaf(f, to[0], y.x);
-                    to[1] = fmaf(f, to[1], y.y);
-                    to[2] = fmaf(f, to[2], y.z);
-                    to[3] = fmaf(f, to[3], y.w);
-                }
-                __syncwarp();
-            }
-        };
         auto store = [&](float *p) {
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
@@ -615,25 +603,47 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 __syncwarp();
             }
         };
-        // S0, by way of the workspace when segments start from it while the last one writes S_new.
         const size_t at = ((size_t)flat * kC + quad * 32) * kC + wg * 64;   // [batch, heads_v, dv] rows are flat 128-row items
-        float *const slots = a.segments > 1 ? a.seg_state + ((size_t)flat * a.segments * kC + quad * 32) * kC + wg * 64 : nullptr;
+        float *const slots = a.segments > 1 ? a.seg_state + ((size_t)flat * (a.segments - 1) * kC + quad * 32) * kC + wg * 64 : nullptr;
 #pragma unroll
         for (int e = 0; e < 64; ++e) st[e] = 0.f;
-        if (kState) {
-            if (seg == 0 && a.S0)              // its own state is taken from zero
+        if (!kState) {
+            // S0, or the first segment's state (S0 is in it) folded with those between: in the order of the loads,
+            // which depend on nothing, then once into rows.  (By way of rows for each: 3 us a segment.)
 #pragma unroll
-                for (int half = 0; half < 2; ++half)
+            for (int half = 0; half < 2; ++half) {
+                float4 sum[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) sum[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                const float *p = seg > 0 ? slots : a.S0 ? a.S0 + at : nullptr;
+                if (p)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) sum[k] = *reinterpret_cast<const float4 *>(p + half * 32 + far(k));
+#pragma unroll 1
+                for (int s = 1; s < seg; ++s) {
+                    const double *lg = a.seg_log + ((size_t)flat * (a.segments - 1) + s) * 4 + h;
+                    float4 x[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) x[k] = *reinterpret_cast<const float4 *>(slots + (size_t)s * kC * kC + half * 32 + far(k));
+                    const float f = exp2f((float)(lg[0] + lg[2]));
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        *reinterpret_cast<float4 *>(slots + half * 32 + far(k)) =
-                            *reinterpret_cast<const float4 *>(a.S0 + at + half * 32 + far(k));
-        } else {
-            if (a.S0) fold(a.segments > 1 ? slots : a.S0 + at, 0.f);
-#pragma unroll 1
-            for (int s = 0; s < seg; ++s) {    // the segments before this one
-                const size_t p = (size_t)flat * (a.segments - 1) + s;
-                fold(slots + (size_t)(s + 1) * kC * kC, exp2f((float)(a.seg_log[p * 4 + h] + a.seg_log[p * 4 + 2 + h])));
+                        sum[k] = make_float4(fmaf(f, sum[k].x, x[k].x), fmaf(f, sum[k].y, x[k].y), fmaf(f, sum[k].z, x[k].z),
+                                             fmaf(f, sum[k].w, x[k].w));
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) *near(k * 4 + row4, col4) = sum[k];
+                __syncwarp();
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const float4 y = *near(lane, c);
+                    float *to = st + half * 32 + c * 4;
+                    to[0] = y.x;
+                    to[1] = y.y;
+                    to[2] = y.z;
+                    to[3] = y.w;
+                }
+                __syncwarp();
             }
             asm volatile("bar.sync 1, 256;" ::: "memory");   // the copy's room is free
         }
@@ -737,8 +747,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             ptx::tc_fence_after();
             take(decay, kColD);
         }
-        float *dst = kState ? slots + (size_t)(seg + 1) * kC * kC
-                            : last && a.S_new ? a.S_new + at : nullptr;
+        float *dst = kState || beside ? slots + (size_t)seg * kC * kC : last && a.S_new ? a.S_new + at : nullptr;
         if (dst && run) store(dst);        // the last Q S^T has read its copy
     }
 
@@ -757,6 +766,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tmem, 512);
     }
+    if (beside) wait_dependency();         // what follows this launch follows the state-only one too
 }
 
 std::mutex g_mutex;
@@ -782,7 +792,7 @@ cudaError_t prepare(int *sms)
     return cudaSuccess;
 }
 
-// Segments of a sequence: as many as fill the SMs with one CTA each, while a segment of a
+// Segments of a sequence: as many as fill the SMs with one CTA each in both passes, while a segment of a
 // sequence of average length has at least four chunks (a CTA's set-up and the first launch
 // cost about two).
 int segments_for(int batch, int total, int items, int sms)
@@ -790,12 +800,12 @@ int segments_for(int batch, int total, int items, int sms)
     int s = sms / (items > 0 ? items : 1);
     const int by_len = total / (batch > 0 ? batch : 1) / (4 * kC);
     s = s < by_len ? s : by_len;
-    return s < 1 ? 1 : s > kMaxSegments ? kMaxSegments : s;
+    return s < 2 ? 1 : s + 1 > kMaxSegments ? kMaxSegments : s + 1;   // the first runs beside the states
 }
 
 size_t workspace_for(int items, int segments)
 {
-    return segments > 1 ? (size_t)items * segments * (kC * kC * sizeof(float) + 4 * sizeof(double)) : 0;
+    return segments > 1 ? (size_t)items * (segments - 1) * (kC * kC * sizeof(float) + 4 * sizeof(double)) : 0;
 }
 
 }  // namespace
@@ -839,22 +849,28 @@ cudaError_t launch_linear_tc(const LinearArgs &l, void *workspace, size_t worksp
     if (!workspace || workspace_bytes < workspace_for(items, a.segments)) a.segments = 1;
     if (a.segments > 1) {
         a.seg_log = static_cast<double *>(workspace);
-        a.seg_state = reinterpret_cast<float *>(a.seg_log + (size_t)items * a.segments * 4);
+        a.seg_state = reinterpret_cast<float *>(a.seg_log + (size_t)items * (a.segments - 1) * 4);
     }
     CUtensorMap q{}, k{}, v{}, o{};
     if (l.total > 0 && (!encode_heads(&q, l.q, l.total, l.heads_k, 1, kC) || !encode_heads(&k, l.k, l.total, l.heads_k, 1, kC) ||
                         !encode_heads(&v, l.v, l.total, a.per_seq, 1, kC) || !encode_heads(&o, l.o, l.total, a.per_seq, 1, 32)))
         return cudaErrorInvalidValue;
     const bool one = l.dv == kC;
-    if (a.segments > 1) {
-        const dim3 grid((unsigned)(items * (a.segments - 1)));
-        e = one ? launch_pdl(linear_tc_kernel<1, true>, grid, kThreads, kSmem, s, q, k, v, o, a)
-                : launch_pdl(linear_tc_kernel<2, true>, grid, kThreads, kSmem, s, q, k, v, o, a);
-        if (e != cudaSuccess) return e;
-    }
-    const dim3 grid((unsigned)(items * a.segments + 1));
-    return one ? launch_pdl(linear_tc_kernel<1, false>, grid, kThreads, kSmem, s, q, k, v, o, a)
-               : launch_pdl(linear_tc_kernel<2, false>, grid, kThreads, kSmem, s, q, k, v, o, a);
+    const auto walk = [&](int first, int count) {
+        a.seg_first = first;
+        a.seg_count = count;
+        const dim3 grid((unsigned)(items * count + (first == 0 ? 1 : 0)));   // and the error word
+        return one ? launch_pdl(linear_tc_kernel<1, false>, grid, kThreads, kSmem, s, q, k, v, o, a)
+                   : launch_pdl(linear_tc_kernel<2, false>, grid, kThreads, kSmem, s, q, k, v, o, a);
+    };
+    if (a.segments == 1) return walk(0, 1);
+    a.seg_first = 1;
+    a.seg_count = a.segments - 2;
+    const dim3 grid((unsigned)(items * a.seg_count));
+    e = one ? launch_pdl(linear_tc_kernel<1, true>, grid, kThreads, kSmem, s, q, k, v, o, a)
+            : launch_pdl(linear_tc_kernel<2, true>, grid, kThreads, kSmem, s, q, k, v, o, a);
+    if (e != cudaSuccess || (e = walk(0, 1)) != cudaSuccess) return e;
+    return walk(1, a.segments - 1);
 }
 
 }  // namespace stree

@@ -12,14 +12,17 @@ namespace stree {
 
 constexpr int kCacheDim = 128;                 // head dim of every cached row
 
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_dependency() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 __device__ __forceinline__ void pdl_start()
 {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    launch_dependents();
+    wait_dependency();
 }
 
 // One launch that may start while its predecessor on the stream drains (every
-// kernel launched this way begins with pdl_start before it touches memory).
+// kernel launched this way begins with pdl_start before it touches memory, or waits where it says).
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, int threads, size_t smem, cudaStream_t s, Args... args)
 {
