@@ -69,6 +69,8 @@ struct PromptArgs {
     __nv_bfloat16 *o;
     int32_t *err;
     int total, batch, heads_q, heads_kv, group, tokens;   // tokens: of a half, 128 / group
+    uint32_t wait_ns;                          // limit of a wait
+    int fault;                                 // test hook: 1 withholds the first part of P of a CTA's first tile
     float scale_log2;
 };
 
@@ -159,8 +161,8 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     const uint32_t q0 = ptx::smem_u32(smem), ring = q0 + 2 * kTile;
     const int tid = threadIdx.x, lane = tid & 31, warp = ptx::warp_index();
 
-    auto wait = [&](int i, uint32_t parity, int where) { return wait_one(&aborted, bar(i), parity, where); };
-    auto warp_wait = [&](int i, uint32_t parity, int where) { return wait_warp(&aborted, bar(i), parity, where); };
+    auto wait = [&](int i, uint32_t parity, int where) { return wait_one(&aborted, bar(i), parity, where, a.wait_ns); };
+    auto warp_wait = [&](int i, uint32_t parity, int where) { return wait_warp(&aborted, bar(i), parity, where, a.wait_ns); };
     if (tid == 0) {
         ptx::prefetch_tensormap(&tm_q);
         ptx::prefetch_tensormap(&tm_k);
@@ -195,6 +197,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     };
 
     int loads = 0, requests = 0, q_loads = 0;
+    bool pending = false;                      // a request of the scheduler whose answer has not been read
     if (warp == 0) {
         if (ptx::elect_one()) {
             // ------------------------------------------------------------ producer
@@ -350,7 +353,9 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                 ptx::clc_request(ptx::smem_u32(&answer), bar(B_NEXT));
             }
             __syncwarp();
+            pending = true;
             if (!(ok = warp_wait(B_NEXT, (uint32_t)requests, 31))) break;
+            pending = false;
             ++requests;
             x = ptx::clc_answer(ptx::smem_u32(&answer));
             __syncwarp();
@@ -434,7 +439,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                     ptx::tmem_wait_st();
                     ptx::tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(bar(B_PF + kParts * half + c));
+                    if (lane == 0 && !(c == 0 && a.fault && k + i == 0)) ptx::mbar_arrive(bar(B_PF + kParts * half + c));
                 }
                 l = l * f + ((sum[0].x + sum[1].x) + (sum[0].y + sum[1].y));
             }
@@ -471,16 +476,19 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     }
 
     // -------------------------------------------------------------------- teardown
-    if (tid == 96 && aborted && a.err) latch_error(a.err, STREE_ERR_TIMEOUT, -1, aborted, 0);
-    if (warp == 0 && aborted && q_loads > 0) {
-        // Copies that may still land.
-        ptx::mbar_wait(bar(B_QF), (uint32_t)((q_loads - 1) & 1));
-#pragma unroll 1
-        for (int x = max(0, loads - kSlots); x < loads; ++x) ptx::mbar_wait(bar(B_F + x % kSlots), (uint32_t)((x / kSlots) & 1));
-    }
-    if (warp == 2 && aborted) ptx::mbar_wait(bar(B_NEXT), (uint32_t)(requests & 1));
     ptx::tc_fence_before();
-    __syncthreads();
+    __syncthreads();                           // all roles have ended: `aborted` no longer changes
+    if (aborted) {
+        if (tid == 0 && a.err) latch_error(a.err, STREE_ERR_TIMEOUT, -1, aborted, 0);
+        // What may still land in shared memory: copies, and an answer that was not waited for.
+        if (q_loads > 0) {                     // the producer's lane
+            ptx::mbar_wait(bar(B_QF), (uint32_t)((q_loads - 1) & 1));
+#pragma unroll 1
+            for (int x = max(0, loads - kSlots); x < loads; ++x) ptx::mbar_wait(bar(B_F + x % kSlots), (uint32_t)((x / kSlots) & 1));
+        }
+        if (pending) ptx::mbar_wait(bar(B_NEXT), (uint32_t)(requests & 1));
+        __syncthreads();
+    }
     if (warp == 1) {
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tmem, 512);
@@ -535,6 +543,9 @@ extern "C" stree_status stree_prompt_attention(const void *q, const void *k, con
     a.group = heads_q / heads_kv;
     a.tokens = kM / a.group;
     a.scale_log2 = scale * 1.4426950408889634f;
+    const WaitHook hook = wait_hook();
+    a.wait_ns = hook.limit_ns;
+    a.fault = hook.fault;
     // Every sequence has at most one tile that it does not fill; no token, no tile.
     const long long tiles = total / (2 * a.tokens) + (batch < total ? batch : total);
     const long long grid = tiles * heads_kv + 1;

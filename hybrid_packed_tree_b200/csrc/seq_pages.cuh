@@ -42,15 +42,16 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, int threads, size_t 
 // The waits of a kernel's warp roles: bounded (about a second), and small, since a copy of the
 // code stands at each of some twenty waits and several roles share the instruction cache.  A
 // wait that runs out leaves its number in `aborted` (a shared int, zero before); every other
-// wait of the CTA then gives up too, and the kernel's end reports it.
-__device__ __forceinline__ bool wait_one(volatile int *aborted, uint32_t bar, uint32_t parity, int where)
+// wait of the CTA then gives up too, and when all roles have ended the kernel reports it.
+__device__ __forceinline__ bool wait_one(volatile int *aborted, uint32_t bar, uint32_t parity, int where,
+                                         uint32_t limit_ns = (uint32_t)ptx::kWaitLimitNs)
 {
     if (ptx::mbar_try_wait(bar, parity & 1)) return true;
     const uint32_t t0 = ptx::globaltimer_lo();
 #pragma unroll 1
     while (!ptx::mbar_try_wait(bar, parity & 1)) {
         if (*aborted) return false;
-        if (ptx::globaltimer_lo() - t0 > (uint32_t)ptx::kWaitLimitNs) {
+        if (ptx::globaltimer_lo() - t0 > limit_ns) {
             *aborted = where;
             return false;
         }
@@ -59,9 +60,10 @@ __device__ __forceinline__ bool wait_one(volatile int *aborted, uint32_t bar, ui
 }
 
 // All lanes of a warp wait together, with one answer.
-__device__ __forceinline__ bool wait_warp(volatile int *aborted, uint32_t bar, uint32_t parity, int where)
+__device__ __forceinline__ bool wait_warp(volatile int *aborted, uint32_t bar, uint32_t parity, int where,
+                                          uint32_t limit_ns = (uint32_t)ptx::kWaitLimitNs)
 {
-    return __all_sync(0xffffffffu, wait_one(aborted, bar, parity, where));
+    return __all_sync(0xffffffffu, wait_one(aborted, bar, parity, where, limit_ns));
 }
 
 // A sequence's packed rows [begin, end); an offset pair that is not ascending

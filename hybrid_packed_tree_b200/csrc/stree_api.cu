@@ -36,6 +36,8 @@ struct stree_ctx {
 
 namespace {
 
+thread_local stree_wait_hook g_wait_hook{0, 0};
+
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 stree_status cuda_status(cudaError_t e) { return e == cudaSuccess ? STREE_OK : STREE_ERR_CUDA; }
@@ -231,6 +233,12 @@ cudaError_t launch_scan(ScanPath path, const ScanArgs &a, cudaStream_t s, int64_
     return cudaErrorInvalidValue;
 }
 
+WaitHook wait_hook()
+{
+    const uint64_t ns = g_wait_hook.wait_ns ? g_wait_hook.wait_ns : 1000000000ull;   // about 1 s
+    return WaitHook{(uint32_t)ns, g_wait_hook.fault};
+}
+
 }  // namespace stree
 
 extern "C" {
@@ -294,6 +302,14 @@ stree_status stree_ctx_set_test_fault(stree_ctx *c, int fault)
 {
     if (!c || fault < 0 || fault > 1) return STREE_ERR_INVALID_ARG;
     c->fault = fault;
+    return STREE_OK;
+}
+
+stree_status stree_set_wait_hook(const stree_wait_hook *hook)
+{
+    // Device time is compared in 32 bits of nanoseconds.
+    if (!hook || hook->fault < 0 || hook->fault > 1 || hook->wait_ns > 4000000000ull) return STREE_ERR_INVALID_ARG;
+    g_wait_hook = *hook;
     return STREE_OK;
 }
 

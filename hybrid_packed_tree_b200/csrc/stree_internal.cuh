@@ -58,6 +58,14 @@ struct ScanArgs {
     int fault;                         // tensor-core kernel: failure-path test hook (0: off)
 };
 
+// What stree_set_wait_hook has set for the calling thread: the limit of a bounded wait in
+// nanoseconds, and whether a call withholds one hand-off between two warp roles (0: no).
+struct WaitHook {
+    uint32_t limit_ns;
+    int fault;
+};
+WaitHook wait_hook();
+
 // The kernels that can run a scan.
 enum class ScanPath { Small, Tc, Simt };
 

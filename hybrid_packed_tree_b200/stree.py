@@ -40,7 +40,7 @@ KERNELS = {"auto": 0, "simt": 1, "tc": 2, "small": 3}
 # Every exported symbol of include/stree.h.
 EXPORTS = (
     "stree_ctx_create", "stree_ctx_destroy", "stree_ctx_set_kernel", "stree_ctx_launch_count",
-    "stree_ctx_last_kernel", "stree_ctx_set_wait_limit", "stree_ctx_set_test_fault",
+    "stree_ctx_last_kernel", "stree_ctx_set_wait_limit", "stree_ctx_set_test_fault", "stree_set_wait_hook",
     "stree_build_tree",
     "stree_tree_scan", "stree_commit", "stree_tree_scan_commit", "stree_tree_scan_commit_noalloc",
     "stree_resolve_path", "stree_unrolled_scan", "stree_accept_greedy", "stree_accept_sampling",
@@ -59,6 +59,7 @@ _lib.stree_ctx_launch_count.argtypes = [_vp, ctypes.POINTER(ctypes.c_int64)]
 _lib.stree_ctx_last_kernel.argtypes = [_vp, ctypes.POINTER(ctypes.c_int)]
 _lib.stree_ctx_set_wait_limit.argtypes = [_vp, ctypes.c_uint64]
 _lib.stree_ctx_set_test_fault.argtypes = [_vp, _i]
+_lib.stree_set_wait_hook.argtypes = [_vp]
 _lib.stree_build_tree.argtypes = [_vp, _vp, _i, _i, _vp, _vp, _vp]
 _lib.stree_tree_scan.argtypes = [_vp] * 9 + [_i] * 7 + [_vp, _vp]
 _lib.stree_commit.argtypes = [_vp, _vp, _vp, _i, _vp, _vp]
@@ -198,6 +199,19 @@ def stree_ctx_set_wait_limit(ctx: Ctx, ns: int = 0):
 def stree_ctx_set_test_fault(ctx: Ctx, fault: int = 0):
     """Failure-path test hook: 1 makes a bounded wait of the tensor-core kernel run out."""
     _check(_lib.stree_ctx_set_test_fault(ctx.handle, int(fault)), "stree_ctx_set_test_fault")
+
+
+class _WaitHook(ctypes.Structure):
+    _fields_ = [("wait_ns", ctypes.c_uint64), ("fault", ctypes.c_int)]
+
+
+def stree_set_wait_hook(wait_ns: int = 0, fault: int = 0):
+    """Bounded-wait limit in ns (0: about 1 s) of the calls without a context that hand work between
+    warp roles, for later calls of this thread; fault=1, a test hook, makes one of their waits run out."""
+    if not 0 <= int(wait_ns) < 1 << 64:
+        raise ValueError("wait_ns must be a number of nanoseconds")
+    hook = _WaitHook(int(wait_ns), int(fault))
+    _check(_lib.stree_set_wait_hook(ctypes.byref(hook)), "stree_set_wait_hook")
 
 
 def stree_build_tree(ctx: Ctx, parent, anc_out=None, depth_out=None, stream=None):

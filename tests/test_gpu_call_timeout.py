@@ -1,0 +1,63 @@
+"""Failure detection of the warp-role kernels without a context, exercised without a GPU fault.
+
+Their waits are bounded.  The test hook withholds one hand-off between two roles, on which no
+copy depends, so that a wait runs out: the call must return, report STREE_ERR_TIMEOUT in the
+error word whichever role gave up, leave what it did not compute untouched, and the next call
+must be exact again.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle.prompt import oracle_prompt_attention
+
+from prompt_util import attention_tol, bf16, f64, i32, offsets, within
+
+pytestmark = pytest.mark.gpu
+
+STREE_ERR_TIMEOUT = 7
+SCALE = 0.09
+
+
+@pytest.fixture(scope="module")
+def st():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from hybrid_packed_tree_b200 import stree
+    return stree
+
+
+@pytest.fixture
+def fault(st):
+    """Runs a call with the hook set: its error word."""
+    def run(call):
+        err = torch.full((4,), -1, dtype=torch.int32, device="cuda")
+        st.stree_set_wait_hook(2_000_000, 1)   # 2 ms
+        try:
+            call(err)
+        finally:
+            st.stree_set_wait_hook()
+        torch.cuda.synchronize()
+        return err.tolist()
+    yield run
+    st.stree_set_wait_hook()
+
+
+@pytest.mark.parametrize("lens", [[1], [97], [300, 0, 5], [700, 650]])
+def test_prompt_attention_reports_a_wait_that_ran_out(st, fault, lens):
+    rng = np.random.default_rng(sum(lens))
+    n = sum(lens)
+    q, k, v = (bf16(rng.normal(size=(n, h, 128))) for h in (4, 2, 2))
+    cu = i32(offsets(lens))
+    o = torch.full_like(q, 7.0)
+    err = fault(lambda e: st.stree_prompt_attention(q, k, v, cu, o, SCALE, err_out=e))
+    assert err[0] == STREE_ERR_TIMEOUT, err
+    assert torch.all(o == 7.0)                 # every CTA gave up at its first tile
+    err = torch.full((4,), -1, dtype=torch.int32, device="cuda")
+    st.stree_prompt_attention(q, k, v, cu, o, SCALE, err_out=err)
+    torch.cuda.synchronize()
+    assert err.tolist() == [0, 0, 0, 0]
+    at = offsets(lens)
+    for lo, hi in zip(at, at[1:]):
+        ref, oa = oracle_prompt_attention(f64(q[lo:hi]), f64(k[lo:hi]), f64(v[lo:hi]), SCALE)
+        within(f64(o[lo:hi]), ref, attention_tol(ref, oa, 40.0), "after the timeout")
