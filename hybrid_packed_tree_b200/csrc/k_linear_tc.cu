@@ -96,6 +96,8 @@ struct TcArgs {
     int32_t *err;
     int total, batch, heads_v, heads_k, per_seq, segments;   // per_seq: 128-column items of a sequence
     int seg_first, seg_count;                  // of this launch
+    uint32_t wait_ns;                          // limit of a wait
+    int fault;                                 // test hook: 1 withholds the first hand-over of a CTA's first chunk
 };
 
 constexpr uint32_t kStage = 4 * 4096;          // rows of O on their way out: 32 rows of 64 columns a warp
@@ -175,10 +177,10 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const bool last = seg == a.segments - 1;
     if (n == 0 && !kState && seg > 0 && !last) return;   // nothing to put out
 
-    auto wait = [&](int i, uint32_t parity, int where) { return wait_one(&aborted, bar(i), parity, where); };
-    auto warp_wait = [&](int i, uint32_t parity, int where) { return wait_warp(&aborted, bar(i), parity, where); };
+    auto wait = [&](int i, uint32_t parity, int where) { return wait_one(&aborted, bar(i), parity, where, a.wait_ns); };
+    auto warp_wait = [&](int i, uint32_t parity, int where) { return wait_warp(&aborted, bar(i), parity, where, a.wait_ns); };
     auto both_wait = [&](int i, uint32_t i_parity, int j, uint32_t j_parity, int where) {
-        const bool ok = wait_one(&aborted, bar(i), i_parity, where) && wait_one(&aborted, bar(j), j_parity, where + 1);
+        const bool ok = wait(i, i_parity, where) && wait(j, j_parity, where + 1);
         return __all_sync(0xffffffffu, ok) != 0;
     };
     if (tid == 0) {
@@ -464,7 +466,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 #pragma unroll 1
                     for (int z = 0; z < 2; ++z) form(i, s * 32 + z * 16, state_col_w(s) + z * 8, 16);
                     formed();
-                    if (lane == 0) ptx::mbar_arrive(bar(B_WF + s));
+                    if (lane == 0 && !(a.fault && i + s == 0)) ptx::mbar_arrive(bar(B_WF + s));
                 }
                 if (!ok) break;
                 if (lane == 0) ptx::mbar_arrive(bar(B_GE + (i & 1)));
@@ -529,7 +531,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 ptx::tmem_wait_st();
                 ptx::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(bar(B_PF));
+                if (lane == 0 && !(a.fault && i == 0)) ptx::mbar_arrive(bar(B_PF));
                 // The output of token r, half a row at a time: by way of shared memory to global memory in
                 // one copy of the warp's 32 rows.  (16-byte stores from the lanes took five times as long, and
                 // a bulk copy for each row as long as those.)  Rows past the sequence's end are another's: the
@@ -752,16 +754,20 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     }
 
     // -------------------------------------------------------------------- teardown
-    if (tid == 96 && aborted && a.err) latch_error(a.err, STREE_ERR_TIMEOUT, b, aborted, 0);
-    if ((warp == 1 || warp == 2) && aborted && ptx::elect_one()) {
-        ptx::mma_commit(bar(B_DRAIN + warp - 1));   // every issued MMA completes first
-        ptx::mbar_wait(bar(B_DRAIN + warp - 1), 0);
-    }
-    if (warp == 0 && aborted && loads > 0)
+    ptx::tc_fence_before();
+    __syncthreads();                           // all roles have ended: `aborted` no longer changes
+    if (aborted) {
+        if (tid == 0 && a.err) latch_error(a.err, STREE_ERR_TIMEOUT, b, aborted, 0);
+        if ((warp == 1 || warp == 2) && ptx::elect_one()) {
+            ptx::mma_commit(bar(B_DRAIN + warp - 1));   // every issued MMA completes first
+            ptx::mbar_wait(bar(B_DRAIN + warp - 1), 0);
+        }
+        // Copies that may still land (`loads`: the producer's lane).
 #pragma unroll 1
         for (int x = max(0, loads - kSlots); x < loads; ++x) ptx::mbar_wait(bar(B_F + x % kSlots), (uint32_t)((x / kSlots) & 1));
-    ptx::tc_fence_before();
-    __syncthreads();
+        ptx::tc_fence_before();
+        __syncthreads();
+    }
     if (warp == 1) {
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tmem, 512);
@@ -844,6 +850,9 @@ cudaError_t launch_linear_tc(const LinearArgs &l, void *workspace, size_t worksp
     a.heads_v = l.heads_v;
     a.heads_k = l.heads_k;
     a.per_seq = l.heads_v * l.dv / kC;
+    const WaitHook hook = wait_hook();
+    a.wait_ns = hook.limit_ns;
+    a.fault = hook.fault;
     const int items = l.batch * a.per_seq;
     a.segments = segments_for(l.batch, l.total, items, sms);
     if (!workspace || workspace_bytes < workspace_for(items, a.segments)) a.segments = 1;

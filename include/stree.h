@@ -137,7 +137,7 @@ stree_status stree_ctx_set_test_fault(stree_ctx *ctx, int fault);
 
 /*
  * The bounded waits of the calls that have no context and hand work between warp roles
- * (stree_prompt_attention), for later calls from the calling thread; a captured call keeps
+ * (stree_linear_prompt on the tensor cores, stree_prompt_attention), for later calls from the calling thread; a captured call keeps
  * what it was captured with.  A wait that runs out latches STREE_ERR_TIMEOUT in the call's
  * err_out; the CTA then does no further work, waits (bounded) for its own copies and MMAs in
  * flight, frees its tensor memory and exits: the call's outputs are incomplete, and the next

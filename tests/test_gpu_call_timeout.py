@@ -9,9 +9,9 @@ import numpy as np
 import pytest
 import torch
 
-from oracle.prompt import oracle_prompt_attention
+from oracle.prompt import oracle_linear, oracle_prompt_attention
 
-from prompt_util import attention_tol, bf16, f64, i32, offsets, within
+from prompt_util import E, U, attention_tol, bf16, f32, f64, i32, offsets, within
 
 pytestmark = pytest.mark.gpu
 
@@ -61,3 +61,33 @@ def test_prompt_attention_reports_a_wait_that_ran_out(st, fault, lens):
     for lo, hi in zip(at, at[1:]):
         ref, oa = oracle_prompt_attention(f64(q[lo:hi]), f64(k[lo:hi]), f64(v[lo:hi]), SCALE)
         within(f64(o[lo:hi]), ref, attention_tol(ref, oa, 40.0), "after the timeout")
+
+
+@pytest.mark.parametrize("dv", [128, 64])
+@pytest.mark.parametrize("lens", [[1], [128, 0, 129], [2300, 1900, 5]])
+def test_linear_prompt_reports_a_wait_that_ran_out(st, fault, lens, dv):
+    """One chunk (the gate warp is done long before another role gives up), several, and the split."""
+    rng = np.random.default_rng(sum(lens))
+    n, b, hv, hk = sum(lens), len(lens), 2, 1
+    q, k = (bf16(rng.normal(size=(n, hk, 128)) / np.sqrt(128)) for _ in range(2))
+    v, alpha, beta = bf16(rng.normal(size=(n, hv, dv))), f32(rng.uniform(0.9, 1.0, size=(n, hv))), f32(rng.uniform(size=(n, hv)))
+    S0, cu = f32(rng.normal(0, 0.3, size=(b, hv, dv, 128))), i32(offsets(lens))
+    ws = torch.full((max(16, st.stree_linear_prompt_workspace_size(b, n, hv, hk, 128, dv)),), 0xFF, dtype=torch.uint8, device="cuda")
+    o, S = torch.full_like(v, 7.0), torch.full_like(S0, 7.0)
+
+    def call(err):
+        st.stree_linear_prompt(q, k, v, alpha, beta, cu, o, S0=S0, S_new=S, err_out=err, workspace=ws)
+
+    err = fault(call)
+    assert err[0] == STREE_ERR_TIMEOUT, err
+    assert torch.all(o == 7.0)                 # every CTA gave up at its first chunk
+    err = torch.full((4,), -1, dtype=torch.int32, device="cuda")
+    call(err)
+    torch.cuda.synchronize()
+    assert err.tolist() == [0, 0, 0, 0]
+    at = offsets(lens)
+    for i, (lo, hi) in enumerate(zip(at, at[1:])):
+        ro, rS, oa, Sa = oracle_linear(*(f64(t[lo:hi]) for t in (q, k, v, alpha, beta)), S0=f64(S0[i]))
+        ops = 2 * (hi - lo) + 128 + 300        # as for the prompts without a timeout
+        within(f64(o[lo:hi]), ro, U * np.abs(ro) + (U + ops * E) * oa + 1e-30, "o after the timeout")
+        within(f64(S[i]), rS, ops * E * Sa + 1e-30, "S after the timeout")
