@@ -75,6 +75,8 @@ struct PagedArgs {
     int batch, heads_q, heads_kv, group, row_tiles, rows;   // rows: min(group, 16)
     int n_pages, page_size, max_pages, blk, box_rows, shares, stages;   // blk: positions per block
     float scale_log2;
+    uint32_t wait_ns;                          // limit of a wait
+    int fault;                                 // test hook: 1 withholds a share's first block
 };
 
 __device__ __forceinline__ int blocks_of(const PagedArgs &a, int b)
@@ -155,6 +157,24 @@ __host__ __device__ constexpr Stage stage_layout()
     return kE4m3 ? Stage{0, 16384, 32768, 32768 + 128, 32768 + 1024} : Stage{0, 16384, 0, 0, 32768};
 }
 
+// What the compute warps do together when a wait of the CTA has run out (the producer gives up
+// too then).  Out of line: inlined it cost the loop registers (bf16, 32 heads over 2: 43 us against 41.3).
+__device__ __noinline__ void give_up(int32_t *err, int b, int where, uint32_t produced, const volatile int *issued_s, uint32_t full0,
+                                            int stages, int fault, float4 *piece, int rows)
+{
+    const int tid = threadIdx.x;
+    ptx::mbar_wait(produced, 0);
+    if (tid == 0) {
+        if (err) latch_error(err, STREE_ERR_TIMEOUT, b, where, 0);
+        // Nothing may still be landing in shared memory when the CTA ends.
+        const int issued = *issued_s;
+        for (int i = max(fault, issued - stages); i < issued; ++i)
+            ptx::mbar_wait(full0 + 8 * (i % stages), (uint32_t)((i / stages) & 1));
+    }
+    // The join leaves rows alone that have a piece in this share.
+    for (int e = tid; e < 2 * rows; e += kComputeWarps * 32) piece[e] = make_float4(0.f, 0.f, 0.f, 1.f);
+}
+
 // NT: tiles of eight query heads in a row of blocks.
 template <bool kE4m3, int NT>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
@@ -165,14 +185,15 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
     constexpr int kHeads = 8 * NT, kBlk = block_positions(kE4m3), KT = kBlk / 64;   // KT: tiles of 16 positions a warp
     constexpr int kEighths = kBlk / 8;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    __shared__ uint64_t bars[2 * kMaxStages];
+    __shared__ uint64_t bars[2 * kMaxStages + 1];
     __shared__ int tmp[33], found[2];
-    __shared__ volatile int aborted, bad[kMaxStages];
+    __shared__ volatile int aborted, issued_s, bad[kMaxStages];
     __shared__ float4 ml_s[kComputeWarps][kHeads];
     uint8_t *smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
     float *joined = reinterpret_cast<float *>(smem + a.stages * L.bytes);   // [4][rows][132]
     auto full = [&](int s) { return ptx::smem_u32(&bars[s]); };
     auto empty = [&](int s) { return ptx::smem_u32(&bars[kMaxStages + s]); };
+    const uint32_t produced = ptx::smem_u32(&bars[2 * kMaxStages]);   // the producer has ended
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
     pdl_start();
@@ -215,6 +236,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
             ptx::mbar_init(full(s), kE4m3 ? 1 + 2 * kEighths : 1);
             ptx::mbar_init(empty(s), kComputeWarps);
         }
+        ptx::mbar_init(produced, 1);
         ptx::fence_mbar_init();
         aborted = 0;
     }
@@ -277,14 +299,15 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
                 }
                 id = lookup();
             }
-            if (lap > 0 && !wait_warp(&aborted, empty(stage), lap - 1, 1)) break;
+            if (lap > 0 && !wait_warp(&aborted, empty(stage), lap - 1, 1, a.wait_ns)) break;
             const int eighth = (lane * (a.box_rows / 8)) & (kEighths - 1);   // of the box that this lane issues
             const int box_id = __shfl_sync(0xffffffffu, cid, eighth), box_row = __shfl_sync(0xffffffffu, crow, eighth);
-            const bool mine = lane < boxes && box_id >= 0;
+            const bool given = !(a.fault && issued == 0);
+            const bool mine = lane < boxes && box_id >= 0 && given;
             const uint32_t n_boxes = __popc(__ballot_sync(0xffffffffu, mine));
             const bool any_bad = __any_sync(0xffffffffu, cid == -1);
             const uint32_t base = ptx::smem_u32(smem) + stage * L.bytes, fb = full(stage);
-            if (lane == 0) {
+            if (lane == 0 && given) {
                 bad[stage] = any_bad;
                 ptx::mbar_expect_tx(fb, n_boxes * box_bytes * (kE4m3 ? 2u : 4u));
             }
@@ -299,7 +322,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
                     ptx::tma_load_2d(at + L.v + 8192, &tm_v, 64, row, fb);
                 }
             }
-            if (kE4m3) {
+            if (kE4m3 && given) {
                 // Half the lanes the eighths of the key scales, half of the value scales.
                 if (cid >= 0)
                     ptx::cp_async8(base + (lane < kEighths ? L.ks : L.vs) + mine8,
@@ -311,15 +334,12 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
                 ++lap;
             }
         }
-        // Nothing may still be landing in shared memory when the CTA ends.
-        if (aborted) {
-            if (lane == 0 && a.err) latch_error(a.err, STREE_ERR_TIMEOUT, b_first, aborted, 0);
-            if (kE4m3) ptx::cp_async_wait_all();
-            if (lane == 0)
-                for (int i = max(0, issued - a.stages); i < issued; ++i)
-                    ptx::mbar_wait(full(i % a.stages), (uint32_t)((i / a.stages) & 1));
+        __syncwarp();
+        if (lane == 0) {
+            issued_s = issued;
+            ptx::mbar_arrive(produced);
         }
-        return;
+        return;                                // early: with it waiting for the others the join's CTAs start late (44.8 us against 41.3)
     }
 
     // ---------------------------------------------------------------- compute
@@ -387,7 +407,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
         int any_bad = 0;
 #pragma unroll 1
         while (true) {
-            if (!(run = wait_warp(&aborted, full(s), phase, 10))) break;
+            if (!(run = wait_warp(&aborted, full(s), phase, 10, a.wait_ns))) break;
             any_bad |= bad[s];
             const uint32_t base = ptx::smem_u32(smem) + s * L.bytes;
             const int key0 = warp * 16 * KT, valid = n - (blk * kBlk + key0);   // positions of this warp that exist
@@ -610,7 +630,10 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
             : "=r"(stop)
             : "r"(run && !aborted ? 0u : 1u), "n"(kComputeWarps * 32)
             : "memory");
-        if (stop) break;
+        if (stop) {
+            give_up(a.err, found[0], aborted, produced, &issued_s, full(0), a.stages, a.fault, a.part_ml + (size_t)blockIdx.x * 2 * a.rows, a.rows);
+            return;
+        }
         piece = 1;
     }
 }
@@ -805,6 +828,9 @@ extern "C" stree_status stree_paged_attention(const void *q, const void *k_pages
     a.page_size = page_size;
     a.max_pages = max_pages;
     a.scale_log2 = scale * 1.4426950408889634f;
+    const WaitHook hook = wait_hook();
+    a.wait_ns = hook.limit_ns;
+    a.fault = hook.fault;
     const int stage = e4m3 ? stage_layout<true>().bytes : stage_layout<false>().bytes;
     const int join = kComputeWarps * a.rows * kJoinRow * (int)sizeof(float), slack = 1024, fixed = 3072;
     a.stages = (kSmemPerCta - join - slack - fixed) / stage;

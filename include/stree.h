@@ -137,11 +137,11 @@ stree_status stree_ctx_set_test_fault(stree_ctx *ctx, int fault);
 
 /*
  * The bounded waits of the calls that have no context and hand work between warp roles
- * (stree_linear_prompt on the tensor cores, stree_prompt_attention), for later calls from the calling thread; a captured call keeps
- * what it was captured with.  A wait that runs out latches STREE_ERR_TIMEOUT in the call's
- * err_out; the CTA then does no further work, waits (bounded) for its own copies and MMAs in
- * flight, frees its tensor memory and exits: the call's outputs are incomplete, and the next
- * call is not affected.
+ * (stree_linear_prompt on the tensor cores, stree_prompt_attention, stree_paged_attention), for
+ * later calls from the calling thread; a captured call keeps what it was captured with.  A wait
+ * that runs out latches STREE_ERR_TIMEOUT in the call's err_out; the CTA then does no further
+ * work, waits (bounded) for its own copies and MMAs in flight, frees its tensor memory and
+ * exits: the call's outputs are incomplete, and the next call is not affected.
  *   wait_ns: limit of a wait in nanoseconds of device time, up to 4 s (0, the default: about 1 s)
  *   fault:   test hook of that path: with 1 every CTA withholds one hand-off (on which no copy
  *            depends) of its first work, so that a wait runs out; 0, the default, turns it off.

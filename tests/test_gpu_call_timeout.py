@@ -9,9 +9,9 @@ import numpy as np
 import pytest
 import torch
 
-from oracle.prompt import oracle_linear, oracle_prompt_attention
+from oracle.prompt import oracle_decode_attention, oracle_linear, oracle_pages, oracle_prompt_attention
 
-from prompt_util import E, U, attention_tol, bf16, f32, f64, i32, offsets, within
+from prompt_util import E, U, attention_tol, bf16, f32, f64, i32, offsets, random_tables, within
 
 pytestmark = pytest.mark.gpu
 
@@ -91,3 +91,37 @@ def test_linear_prompt_reports_a_wait_that_ran_out(st, fault, lens, dv):
         ops = 2 * (hi - lo) + 128 + 300        # as for the prompts without a timeout
         within(f64(o[lo:hi]), ro, U * np.abs(ro) + (U + ops * E) * oa + 1e-30, "o after the timeout")
         within(f64(S[i]), rS, ops * E * Sa + 1e-30, "S after the timeout")
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("lens,hq", [([1], 4), ([40, 0, 5], 8), ([9000, 700], 24)])
+def test_paged_attention_reports_a_wait_that_ran_out(st, fault, lens, hq, cache):
+    """Shares that fit in the ring of stages (the producer is done when the others give up) and longer ones."""
+    rng = np.random.default_rng(sum(lens) + hq)
+    hkv, page = 2, 16
+    table, n_pages = random_tables(rng, lens, page)
+    pages, scales, values = [], [], []
+    for _ in range(2):
+        x = bf16(rng.normal(size=(n_pages, hkv, page, 128)))
+        pages.append(x if cache == "bf16" else x.float().to(torch.float8_e4m3fn))
+        scales.append(None if cache == "bf16" else torch.full((n_pages, hkv, page), 127, dtype=torch.uint8, device="cuda"))
+        values.append(f64(pages[-1].float()))
+    q = bf16(rng.normal(size=(len(lens), hq, 128)))
+    ws = torch.full((st.stree_paged_attention_workspace_size(hq, hkv),), 0xFF, dtype=torch.uint8, device="cuda")
+    o, tab, n = torch.full_like(q, 7.0), i32(table), i32(lens)
+
+    def call(err):
+        st.stree_paged_attention(q, *pages, tab, n, o, SCALE, k_scales=scales[0], v_scales=scales[1], err_out=err, workspace=ws)
+
+    err = fault(call)
+    assert err[0] == STREE_ERR_TIMEOUT, err
+    for b, length in enumerate(lens):          # every share gave up at its first block
+        assert torch.all(o[b] == (7.0 if length else 0.0))
+    err = torch.full((4,), -1, dtype=torch.int32, device="cuda")
+    call(err)
+    torch.cuda.synchronize()
+    assert err.tolist() == [0, 0, 0, 0]
+    for b, length in enumerate(lens):
+        k, v = (oracle_pages(x, table[b], length) for x in values)
+        ref, oa = oracle_decode_attention(f64(q[b]), k, v, SCALE)
+        within(f64(o[b]), ref, attention_tol(ref, oa, 40.0), "after the timeout")
