@@ -156,16 +156,19 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const bool beside = !kState && a.segments > 1 && a.seg_first == 0;
     if (!beside) wait_dependency();
     launch_dependents();
-    if (!kState && a.seg_first == 0 && blockIdx.x == gridDim.x - 1) {   // the error word
+    // The error word, by the first block of a call's first launch: cleared before any wait of the call can run
+    // out.  (By the last block it was cleared when the first CTAs had ended, with what they had reported.)
+    const bool first = kState || (a.seg_first == 0 && a.segments == 1);
+    if (first && blockIdx.x == 0) {
         PageCheck c{};
         c.cu = a.cu;
         c.batch = a.batch;
         c.total = a.total;
         check_pages(c, a.err);
-        if (beside) wait_dependency();
         return;
     }
-    const int seg = a.seg_first + blockIdx.x % a.seg_count, flat = blockIdx.x / a.seg_count;   // flat: (sequence, 128-column item)
+    const int nth = blockIdx.x - (first ? 1 : 0);
+    const int seg = a.seg_first + nth % a.seg_count, flat = nth / a.seg_count;   // flat: (sequence, 128-column item)
     const int item = flat % a.per_seq, b = flat / a.per_seq;
     const int head0 = item * NH, g = head0 / (a.heads_v / a.heads_k);
     const int2 seq = seq_range(a.cu, b, a.total);
@@ -868,14 +871,14 @@ cudaError_t launch_linear_tc(const LinearArgs &l, void *workspace, size_t worksp
     const auto walk = [&](int first, int count) {
         a.seg_first = first;
         a.seg_count = count;
-        const dim3 grid((unsigned)(items * count + (first == 0 ? 1 : 0)));   // and the error word
+        const dim3 grid((unsigned)(items * count + (a.segments == 1 ? 1 : 0)));   // and the error word
         return one ? launch_pdl(linear_tc_kernel<1, false>, grid, kThreads, kSmem, s, q, k, v, o, a)
                    : launch_pdl(linear_tc_kernel<2, false>, grid, kThreads, kSmem, s, q, k, v, o, a);
     };
     if (a.segments == 1) return walk(0, 1);
     a.seg_first = 1;
     a.seg_count = a.segments - 2;
-    const dim3 grid((unsigned)(items * a.seg_count));
+    const dim3 grid((unsigned)(items * a.seg_count + 1));   // and the error word
     e = one ? launch_pdl(linear_tc_kernel<1, true>, grid, kThreads, kSmem, s, q, k, v, o, a)
             : launch_pdl(linear_tc_kernel<2, true>, grid, kThreads, kSmem, s, q, k, v, o, a);
     if (e != cudaSuccess || (e = walk(0, 1)) != cudaSuccess) return e;

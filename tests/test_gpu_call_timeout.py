@@ -125,3 +125,25 @@ def test_paged_attention_reports_a_wait_that_ran_out(st, fault, lens, hq, cache)
         k, v = (oracle_pages(x, table[b], length) for x in values)
         ref, oa = oracle_decode_attention(f64(q[b]), k, v, SCALE)
         within(f64(o[b]), ref, attention_tol(ref, oa, 40.0), "after the timeout")
+
+
+@pytest.mark.parametrize("more", [0, 40])
+def test_linear_prompt_keeps_what_its_first_blocks_report(st, fault, more):
+    """As many CTAs as SMs give up, and more wait behind them: the block that clears the error word does not."""
+    n = torch.cuda.get_device_properties(0).multi_processor_count + more
+    rng = np.random.default_rng(n)
+    q, k, v = (bf16(rng.normal(size=(n, 1, 128))) for _ in range(3))
+    alpha, cu = f32(np.ones((n, 1))), i32(np.minimum(np.arange(n + 1), n - more))    # the last are empty
+    o = torch.full_like(v, 7.0)
+    err = fault(lambda e: st.stree_linear_prompt(q, k, v, alpha, None, cu, o, err_out=e))
+    assert err[0] == STREE_ERR_TIMEOUT, err
+    assert torch.all(o == 7.0)
+    err = torch.full((4,), -1, dtype=torch.int32, device="cuda")
+    st.stree_linear_prompt(q, k, v, alpha, None, cu, o, err_out=err)
+    torch.cuda.synchronize()
+    assert err.tolist() == [0, 0, 0, 0]
+    ref = (f64(q) * f64(k)).sum(-1, keepdims=True) * f64(v)                          # one token each, from no state
+    oa = (np.abs(f64(q)) * np.abs(f64(k))).sum(-1, keepdims=True) * np.abs(f64(v))
+    rows = n - more
+    within(f64(o[:rows]), ref[:rows], (U * np.abs(ref) + (U + 430 * E) * oa + 1e-30)[:rows], "after the timeout")
+    assert torch.all(o[rows:] == 7.0)
