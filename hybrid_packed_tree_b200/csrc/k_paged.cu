@@ -71,6 +71,9 @@ struct PagedArgs {
     float *part_o;                             // [share][2][rows][128]
     float4 *part_ml;                           // [share][2][rows]: (output's reference, sum's reference, sum,
                                                // nonzero: a page out of range)
+    int *gave_up;                              // [share]: the wait that ran out there, or 0; the join reports it.  (The
+                                               // shares cannot: the word is cleared by a block that starts when the
+                                               // first of them have ended.)
     int32_t *err;
     int batch, heads_q, heads_kv, group, row_tiles, rows;   // rows: min(group, 16)
     int n_pages, page_size, max_pages, blk, box_rows, shares, stages;   // blk: positions per block
@@ -159,13 +162,13 @@ __host__ __device__ constexpr Stage stage_layout()
 
 // What the compute warps do together when a wait of the CTA has run out (the producer gives up
 // too then).  Out of line: inlined it cost the loop registers (bf16, 32 heads over 2: 43 us against 41.3).
-__device__ __noinline__ void give_up(int32_t *err, int b, int where, uint32_t produced, const volatile int *issued_s, uint32_t full0,
-                                            int stages, int fault, float4 *piece, int rows)
+__device__ __noinline__ void give_up(int *report, int where, uint32_t produced, const volatile int *issued_s, uint32_t full0,
+                                     int stages, int fault, float4 *piece, int rows)
 {
     const int tid = threadIdx.x;
     ptx::mbar_wait(produced, 0);
     if (tid == 0) {
-        if (err) latch_error(err, STREE_ERR_TIMEOUT, b, where, 0);
+        *report = where;
         // Nothing may still be landing in shared memory when the CTA ends.
         const int issued = *issued_s;
         for (int i = max(fault, issued - stages); i < issued; ++i)
@@ -224,7 +227,10 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
     }
     const long long total = (long long)n_all * per_seq;
     const int shares = (int)min((long long)a.shares, total);   // no share is empty
-    if ((int)blockIdx.x >= shares) return;
+    if ((int)blockIdx.x >= shares) {
+        if (tid == 0) a.gave_up[blockIdx.x] = 0;
+        return;
+    }
     const long long begin = share_begin(total, blockIdx.x, shares), end = share_begin(total, blockIdx.x + 1, shares);
     // The list is ordered by sequence, then by (key/value head, row tile), then by block.
     block_find(a.batch, (int)(begin / per_seq), [&](int b) { return blocks_of(a, b); }, tmp, found);
@@ -631,11 +637,13 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
             : "r"(run && !aborted ? 0u : 1u), "n"(kComputeWarps * 32)
             : "memory");
         if (stop) {
-            give_up(a.err, found[0], aborted, produced, &issued_s, full(0), a.stages, a.fault, a.part_ml + (size_t)blockIdx.x * 2 * a.rows, a.rows);
+            give_up(a.gave_up + blockIdx.x, aborted, produced, &issued_s, full(0), a.stages, a.fault,
+                    a.part_ml + (size_t)blockIdx.x * 2 * a.rows, a.rows);
             return;
         }
         piece = 1;
     }
+    if (tid == 0) a.gave_up[blockIdx.x] = 0;
 }
 
 // Joins the pieces of every row of blocks that more than one share holds.  One block per
@@ -652,6 +660,14 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const Pa
     pdl_start();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per_seq = a.heads_kv * a.row_tiles;
+    // What the shares report, by a block without a row of its own (beside a row's work it took 20 registers more: 70 us
+    // against 67.5 for the e4m3 batch).
+    if (blockIdx.x == gridDim.x - 1) {
+        if (a.err)
+            for (int c = tid; c < a.shares; c += kCombineThreads)
+                if (const int where = a.gave_up[c]) latch_error(a.err, STREE_ERR_TIMEOUT, -1, where, c);
+        return;
+    }
     const int item = blockIdx.x % per_seq, b = blockIdx.x / per_seq;
     int n_all = 0;
     for (int b0 = 0; b0 < a.batch; b0 += kCombineThreads) {
@@ -752,7 +768,7 @@ cudaError_t prepare(int *sms)
 
 bool heads_ok(int heads_q, int heads_kv) { return heads_q >= 1 && heads_kv >= 1 && heads_q % heads_kv == 0; }
 
-size_t paged_ws(int shares, int rows) { return (size_t)shares * 2 * rows * (kD * sizeof(float) + sizeof(float4)); }
+size_t paged_ws(int shares, int rows) { return (size_t)shares * (2 * rows * (kD * sizeof(float) + sizeof(float4)) + sizeof(int)); }
 
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -797,7 +813,7 @@ extern "C" stree_status stree_paged_attention(const void *q, const void *k_pages
     const bool e4m3 = cache_dtype == STREE_E4M3;
     a.blk = block_positions(e4m3);
     const long long blocks = ((long long)max_pages * page_size + a.blk - 1) / a.blk;
-    if (blocks * batch > 0x7fffffffLL || (long long)batch * heads_kv * a.row_tiles > 0x7fffffffLL)
+    if (blocks * batch > 0x7fffffffLL || (long long)batch * heads_kv * a.row_tiles >= 0x7fffffffLL)
         return STREE_ERR_UNSUPPORTED;
     int sms = 0;
     if (prepare(&sms) != cudaSuccess) return STREE_ERR_CUDA;
@@ -820,6 +836,7 @@ extern "C" stree_status stree_paged_attention(const void *q, const void *k_pages
     a.o = static_cast<__nv_bfloat16 *>(o);
     a.part_o = static_cast<float *>(workspace);
     a.part_ml = reinterpret_cast<float4 *>(a.part_o + (size_t)a.shares * 2 * a.rows * kD);
+    a.gave_up = reinterpret_cast<int *>(a.part_ml + (size_t)a.shares * 2 * a.rows);
     a.err = err_out;
     a.batch = batch;
     a.heads_q = heads_q;
@@ -841,7 +858,7 @@ extern "C" stree_status stree_paged_attention(const void *q, const void *k_pages
                              : (nt == 1 ? paged_attention_kernel<false, 1> : paged_attention_kernel<false, 2>);
     const cudaError_t e = launch_pdl(kernel, dim3((unsigned)a.shares + 1), kThreads, smem, s, m_k, m_v, a);
     if (e != cudaSuccess) return STREE_ERR_CUDA;
-    return launch_pdl(paged_combine_kernel, dim3((unsigned)(batch * heads_kv * a.row_tiles)), kCombineThreads, 0, s, a) ==
+    return launch_pdl(paged_combine_kernel, dim3((unsigned)(batch * heads_kv * a.row_tiles) + 1), kCombineThreads, 0, s, a) ==
                    cudaSuccess
                ? STREE_OK
                : STREE_ERR_CUDA;

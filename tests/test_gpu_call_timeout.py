@@ -147,3 +147,23 @@ def test_linear_prompt_keeps_what_its_first_blocks_report(st, fault, more):
     rows = n - more
     within(f64(o[:rows]), ref[:rows], (U * np.abs(ref) + (U + 430 * E) * oa + 1e-30)[:rows], "after the timeout")
     assert torch.all(o[rows:] == 7.0)
+
+
+def test_paged_attention_keeps_what_its_first_blocks_report(st, fault):
+    """More sequences than CTAs fit on the GPU: every CTA gives up, and the block that clears the error word is not the last."""
+    n = 3 * torch.cuda.get_device_properties(0).multi_processor_count
+    rng = np.random.default_rng(n)
+    pages = [bf16(rng.normal(size=(n, 1, 8, 128))) for _ in range(2)]
+    q, table, lens = bf16(rng.normal(size=(n, 2, 128))), i32(np.arange(n)[:, None]), i32(np.full(n, 8))
+    ws = torch.full((st.stree_paged_attention_workspace_size(2, 1),), 0xFF, dtype=torch.uint8, device="cuda")
+    o = torch.full_like(q, 7.0)
+    err = fault(lambda e: st.stree_paged_attention(q, *pages, table, lens, o, SCALE, err_out=e, workspace=ws))
+    assert err[0] == STREE_ERR_TIMEOUT, err
+    assert torch.all(o == 7.0)
+    err = torch.full((4,), -1, dtype=torch.int32, device="cuda")
+    st.stree_paged_attention(q, *pages, table, lens, o, SCALE, err_out=err, workspace=ws)
+    torch.cuda.synchronize()
+    assert err.tolist() == [0, 0, 0, 0]
+    for b in range(n):
+        ref, oa = oracle_decode_attention(f64(q[b]), f64(pages[0][b]).transpose(1, 0, 2), f64(pages[1][b]).transpose(1, 0, 2), SCALE)
+        within(f64(o[b]), ref, attention_tol(ref, oa, 40.0), "after the timeout")
