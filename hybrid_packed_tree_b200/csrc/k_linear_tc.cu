@@ -57,7 +57,9 @@ constexpr int kThreads = 512;
 __host__ __device__ constexpr int ring_slots(bool state) { return state ? 6 : 5; }
 constexpr int kMaxSlots = 6;
 constexpr uint32_t kTile = 128 * 128 * 2, kHalf = kTile / 2;
-constexpr float kLogZero = -130.f;             // log2 of a decay of zero: 2^-130 is flushed to zero
+// log2 of a decay of zero.  The least float is 2^-149, so that 2^kLogZero is zero however it is formed; and no further
+// down, since sums of it within a chunk are rounded to floats.  (2^-130, as exp2f gives it, left 7e-40 of a state.)
+constexpr float kLogZero = -160.f;
 constexpr int kMaxSegments = 9;
 // Length of the first segment to the others': a chunk of the whole walk takes 4.3 us, of the state alone 2.4.
 constexpr int kFirstWeight = 9, kOtherWeight = 16;
