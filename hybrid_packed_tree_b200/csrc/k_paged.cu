@@ -22,11 +22,14 @@
 // stay in registers as the next product's operand; a 128-row tcgen05 tile would be at
 // most one eighth full and adds a round trip through tensor memory for each block.
 // 8-bit pages: keys and values become fp16 exactly (every e4m3 is one).  A query row is
-// scaled to [-1, 1] by a power of two so that it is fp16 as well (an element below 2^-14 of
-// the row's largest loses bits that the fp32 sum would not keep either).  A key's scale
+// scaled to [-2^15, 2^15] by a power of two so that it is fp16 as well, exactly down to 2^-31 of
+// the row's largest element (below, to 2^-40 of it; scaled to [-1, 1], elements below 2^-16 lost bits that
+// decide a score where the keys are zero in the strong channels).  A key's scale
 // multiplies its score; a value's scale 2^e joins its probability before that is rounded to
-// fp16, so the sum has a reference of its own, the maximum of score + e: the largest weight is 1
-// and none overflows, whatever the scales.  (Values widened to bf16 with the scale on a bf16
+// fp16, so the sum has a reference of its own, the maximum of score + e less 15: the largest weight is
+// 2^15, none overflows whatever the scales, and a weight has fp16's eleven bits down to 2^-29 of the largest
+// and is gone below 2^-40.  (With a largest weight of 1 those were 2^-14 and 2^-25: a key that takes nearly all
+// of the softmax with a value near zero left nothing of the others.)  (Values widened to bf16 with the scale on a bf16
 // probability: 120 us; so and with page positions followed without divisions 93; with the keys as
 // the instruction's rows for up to eight heads, below, 60.)
 //
@@ -58,6 +61,7 @@ constexpr int kThreads = (kComputeWarps + 1) * 32;
 constexpr int kMaxHeads = 16;                  // query heads in a row of blocks
 constexpr int kJoinRow = kD + 4;               // floats of a row in shared memory (no bank conflicts)
 constexpr int kMaxStages = 8;
+constexpr int kLift = 15;                      // 8-bit pages: log2 of the largest scaled query element and weight
 
 constexpr int kCtasPerSm = 2;
 constexpr int kSmemPerCta = 226 * 1024 / kCtasPerSm;
@@ -384,10 +388,10 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
                 for (int kk = 0; kk < 8; ++kk) top = max(top, max(finite_top2(qf[t][kk][0]), finite_top2(qf[t][kk][1])));
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                // The row's largest magnitude lies in [2^(e-127), 2^(e-126)).
-                const uint32_t e = min(max(top >> 7, 2u), 252u);
-                const float inv = power_of_two(253u - e);
-                f *= power_of_two(e + 1u);
+                // The row's largest magnitude lies in [2^(e-127), 2^(e-126)); both factors are normal numbers.
+                const uint32_t e = max(top >> 7, (uint32_t)kLift);
+                const float inv = power_of_two(253u + kLift - e);
+                f *= power_of_two(e + 1u - kLift);
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
 #pragma unroll
@@ -494,7 +498,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
                             if (kE4m3) rn[i] = fmaxf(rn[i], __shfl_xor_sync(0xffffffffu, rn[i], d));
                         }
                         mn[i] = fmaxf(m[t][i], mn[i]);
-                        rn[i] = kE4m3 ? fmaxf(ref[t][i], rn[i]) : mn[i];
+                        rn[i] = kE4m3 ? fmaxf(ref[t][i], rn[i] - (float)kLift) : mn[i];
                     }
                     if (__any_sync(0xffffffffu, mn[0] > m[t][0] || mn[1] > m[t][1] || rn[0] > ref[t][0] || rn[1] > ref[t][1])) {
 #pragma unroll
@@ -581,7 +585,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
             if (left > 0) advance();
             if (last) break;
         }
-        // Join the four warps: each leaves its rows, then a thread takes one column.
+        // Join the four warps: each leaves its rows, then a thread takes one column.  The lift ends here.
+        constexpr float kLifted = kE4m3 ? (float)kLift : 0.f, kLower = kE4m3 ? 1.f / (1 << kLift) : 1.f;
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -590,7 +595,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
                 for (int d = 4; d < 32; d <<= 1) l[t][i] += __shfl_xor_sync(0xffffffffu, l[t][i], d);
                 const int r = t * 8 + 2 * t4 + i;
                 if (r >= rows) continue;
-                if (r4 == 0) ml_s[warp][r] = make_float4(ref[t][i], m[t][i], l[t][i], 0.f);
+                if (r4 == 0) ml_s[warp][r] = make_float4(ref[t][i] + kLifted, m[t][i], l[t][i], 0.f);
                 float *dst = joined + ((size_t)warp * a.rows + r) * kJoinRow;
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
@@ -615,7 +620,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
 #pragma unroll
                 for (int w = 0; w < kComputeWarps; ++w) {
                     const float4 ml = ml_s[w][r];
-                    x = fmaf(weight(ml.x, R), joined[((size_t)w * a.rows + r) * kJoinRow + tid], x);
+                    x = fmaf(weight(ml.x, R) * kLower, joined[((size_t)w * a.rows + r) * kJoinRow + tid], x);
                     den = fmaf(weight(ml.y, M), ml.z, den);
                 }
                 if (!whole) {

@@ -501,9 +501,10 @@ stree_status stree_prompt_attention(const void *q, const void *k, const void *v,
  * q, o [batch, heads_q, 128] bf16; seq_len device int32 [batch], clamped to [0, max_pages
  * page_size]; a sequence with no position gives zeros.  A sequence with a page out of
  * range among those it uses keeps its o untouched.  Any number of query heads per
- * key/value head; scale > 0.  fp32 scores, softmax and sums; P (times the value's scale
- * with e4m3 pages) rounded to bf16.  workspace: stree_paged_attention_workspace_size()
- * bytes, 16-byte aligned, required.
+ * key/value head; scale > 0.  fp32 scores, softmax and sums.  bf16 pages: P rounded to bf16.
+ * e4m3 pages: q, scaled by a power of two for each row, and P, times the value's scale, are
+ * rounded to fp16 (eleven bits down to 2^-29 of the largest, nothing below 2^-40 of it).
+ * workspace: stree_paged_attention_workspace_size() bytes, 16-byte aligned, required.
  */
 stree_status stree_paged_attention(const void *q, const void *k_pages, const void *v_pages, const uint8_t *k_scales,
                                    const uint8_t *v_scales, const int32_t *page_table, const int32_t *seq_len,
