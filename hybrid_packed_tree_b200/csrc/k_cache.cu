@@ -105,8 +105,7 @@ __global__ void __launch_bounds__(kThreads) cache_kernel(const CacheArgs a)
         c.n_pages = a.n_pages;
         c.page_size = a.page_size;
         c.max_pages = a.max_pages;
-        c.clamp = kMode == kRead ? (int)min((long long)a.ctx_cap, (long long)a.max_pages * a.page_size)
-                                 : kMode == kCommit ? a.maxlen : -1;
+        c.clamp = kMode == kRead ? a.ctx_cap : kMode == kCommit ? a.maxlen : -1;
         check_pages(c, a.err);
         if (kMode == kCommit && a.err)
             for (int i = threadIdx.x; i < a.batch * a.maxlen; i += kThreads) {

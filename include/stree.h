@@ -548,7 +548,7 @@ stree_status stree_cache_commit(const void *k_tree, const void *v_tree, const in
  * Reads pages back into the contiguous cache of stree_tree_attention: positions
  * j < seq_len[b] (clamped to [0, ctx_cap]) of k_ctx, v_ctx [batch, ctx_cap, heads_kv, 128]
  * bf16; later positions are left as they were, and so is a position whose page is out
- * of range.  Exact: every e4m3 value times its scale (within [9, 246]) is a bf16.
+ * of range or that does not fit max_pages pages (both latch STREE_ERR_BAD_PAGE).  Exact: every e4m3 value times its scale (within [9, 246]) is a bf16.
  */
 stree_status stree_cache_read(const void *k_pages, const void *v_pages, const uint8_t *k_scales,
                               const uint8_t *v_scales, const int32_t *page_table, const int32_t *seq_len, int batch,
