@@ -1,10 +1,12 @@
-"""Build ``libstree.so`` (the C ABI of include/stree.h) in-tree with nvcc for sm_100a, and
-``_bind.so`` (the binding's argument check, csrc/bind.cpp) with g++.
+"""Build ``libstree.so`` (the C ABI of include/stree.h) in-tree with nvcc for sm_100a, and the
+binding's argument check (csrc/bind.cpp) with g++ against the installed torch.
 
     python -m hybrid_packed_tree_b200.build [--force] [--verbose]
 
 Both are written next to this file so that they travel with the source
-tree; nothing is installed into site-packages.
+tree; nothing is installed into site-packages.  The check's file is named after the torch and
+the Python that it was compiled for, and is not needed: where there is none for the present ones
+(and no compiler or headers to make it) the binding checks its arguments in Python.
 """
 from __future__ import annotations
 
@@ -14,13 +16,13 @@ import os
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libstree.so")
-BIND = os.path.join(PKG, "_bind.so")
 BIND_SRC = os.path.join(CSRC, "bind.cpp")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
@@ -40,25 +42,42 @@ def is_stale() -> bool:
     return any(os.path.getmtime(p) > t for p in _deps())
 
 
-def build_bind(force: bool = False) -> str:
-    """Compile csrc/bind.cpp against the installed torch into _bind.so; returns its path."""
-    if not force and os.path.exists(BIND) and os.path.getmtime(BIND) >= os.path.getmtime(BIND_SRC):
-        return BIND
+def bind_path() -> str:
+    """Where the argument check for this torch and this Python is, or would be."""
     import torch
+    tag = f"{torch.__version__}-abi{int(torch.compiled_with_cxx11_abi())}"
+    return os.path.join(PKG, f"_bind.torch-{tag}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
+def build_bind(force: bool = False) -> str:
+    """Compile csrc/bind.cpp against the installed torch; returns bind_path()."""
+    import torch
+    bind = bind_path()
+    if not force and os.path.exists(bind) and os.path.getmtime(bind) >= os.path.getmtime(BIND_SRC):
+        return bind
     at = os.path.dirname(torch.__file__)
-    tmp = BIND + f".tmp{os.getpid()}"
+    tmp = bind + f".tmp{os.getpid()}"
     subprocess.run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
                     f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
                     "-I", sysconfig.get_paths()["include"], "-I", os.path.join(at, "include"),
                     "-I", os.path.join(at, "include", "torch", "csrc", "api", "include"), "-o", tmp, BIND_SRC,
                     "-L", os.path.join(at, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10"], check=True)
-    os.replace(tmp, BIND)
-    return BIND
+    os.replace(tmp, bind)
+    return bind
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile every .cu under csrc/ into libstree.so, and _bind.so; returns the library's path."""
-    build_bind(force)
+    """Compile every .cu under csrc/ into libstree.so, and the argument check; returns the library's path."""
+    build_lib(force, verbose)
+    try:
+        build_bind(force)
+    except (ImportError, OSError, subprocess.CalledProcessError) as e:
+        warnings.warn(f"csrc/bind.cpp was not compiled ({e}); arguments are checked in Python, about 3 us a call slower")
+    return LIB
+
+
+def build_lib(force: bool = False, verbose: bool = False) -> str:
+    """Compile every .cu under csrc/ into libstree.so; returns its path."""
     if not force and not is_stale():
         return LIB
     nvcc = os.environ.get("NVCC", "nvcc")

@@ -4,7 +4,8 @@ Argument marshalling only: shapes are read from the torch tensors, pointers are
 passed as they are, and every step of the scan runs in the library's CUDA
 kernels.  Importing this module loads the library and raises ImportError when it
 has not been built (``python -m hybrid_packed_tree_b200.build``); there is no
-fallback of any kind.
+fallback for a kernel.  The argument check in C++ is an addition to the one here and is
+taken when it has been compiled for the running torch and Python.
 
 The functions carry the C names.  Tensors must be contiguous CUDA tensors in the
 layouts of the header: x [b,T,H,P], dt [b,T,H], A/D [H] fp32, B/C [b,T,G,N],
@@ -14,17 +15,17 @@ path_len [b] int32.  ``stream`` defaults to torch's current stream.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
+import warnings
 
 import torch
 
-from .build import BIND, LIB
+from .build import LIB, bind_path
 
-for _path in (LIB, BIND):
-    if not os.path.exists(_path):
-        raise ImportError(f"{os.path.basename(_path)} is not built ({_path}); run `python -m hybrid_packed_tree_b200.build`")
-
-from . import _bind  # noqa: E402
+if not os.path.exists(LIB):
+    raise ImportError(f"libstree.so is not built ({LIB}); run `python -m hybrid_packed_tree_b200.build`")
 
 _lib = ctypes.CDLL(LIB)
 
@@ -393,7 +394,7 @@ def stree_tree_attention(q, k_ctx, v_ctx, k_tree, v_tree, ctx_len, parent, o, sc
 # ---------------------------------------------------------------- prompts, single tokens, the paged cache
 #
 # A decode step makes several of these calls per layer and token, so their tensors are checked in
-# C++ (csrc/bind.cpp) and their pointers are plain integers.
+# C++ (csrc/bind.cpp, where it has been compiled) and their pointers are plain integers.
 
 _F32, _BF16, _I32, _U8, _E4M3 = torch.float32, torch.bfloat16, torch.int32, torch.uint8, torch.float8_e4m3fn
 _IO = {torch.float32: STREE_F32, torch.bfloat16: STREE_BF16}
@@ -415,9 +416,38 @@ def _refuse(t, name, shape, dtype, dev):
 
 # _arg(t, name, shape, dtype, dev): the pointer of a tensor of exactly this shape and dtype, contiguous, on
 # CUDA device `dev` (_opt: or None); otherwise _refuse says what is wrong.  Asked property by property in
-# Python, a single-token call cost 9.4 us on the host, so 6.5.
-_bind.on_refusal(_refuse)
-_arg, _opt = _bind.arg, _bind.opt
+# Python, as here, a single-token call cost 9.4 us on the host, by csrc/bind.cpp 6.5.
+def _arg(t, name, shape, dtype, dev):
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda and t.get_device() == dev and
+            t.layout is torch.strided and t.is_contiguous()):
+        return t.data_ptr()
+    _refuse(t, name, shape, dtype, dev)
+
+
+def _opt(t, name, shape, dtype, dev):
+    return None if t is None else _arg(t, name, shape, dtype, dev)
+
+
+def _load_bind():
+    """The check that was compiled for this torch and this Python, or None."""
+    path = bind_path()
+    if not os.path.exists(path):
+        return None
+    name = __package__ + "._bind"
+    loader = importlib.machinery.ExtensionFileLoader(name, path)
+    try:
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader(name, loader))
+        loader.exec_module(module)
+    except ImportError as e:
+        warnings.warn(f"{path} does not load ({e}); arguments are checked in Python")
+        return None
+    module.on_refusal(_refuse)
+    return module
+
+
+_bind = _load_bind()
+if _bind is not None:
+    _arg, _opt = _bind.arg, _bind.opt
 
 
 def _call(where, fn, dev, stream, *args):
