@@ -49,20 +49,6 @@ __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes)
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 
-// Whether a phase is complete, without waiting.
-__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
 // The thread may be suspended in the instruction (for a time the hardware
 // chooses) until the phase completes, so a waiting warp does not take issue slots
 // from working ones.  (An explicit suspend-time hint measured slower: waking
@@ -428,7 +414,6 @@ __device__ __forceinline__ void tmem_ld128(uint32_t taddr, uint32_t (&r)[128])
         : "memory");
 }
 
-// 2^x by the hardware approximation (ex2.approx.ftz.f32; -inf gives +0).
 // 32 bytes to a 32-byte boundary.
 __device__ __forceinline__ void st_global_32b(void *p, const uint32_t *w)
 {
@@ -437,6 +422,7 @@ __device__ __forceinline__ void st_global_32b(void *p, const uint32_t *w)
                  : "memory");
 }
 
+// 2^x by the hardware approximation (ex2.approx.ftz.f32; -inf gives +0).
 __device__ __forceinline__ float ex2_approx(float x)
 {
     float y;
