@@ -18,8 +18,10 @@
 //
 // Precision.  P and the copy of S that Q multiplies are rounded to bf16 (they only enter o,
 // itself bf16).  The state is kept in fp32 registers and receives w_j v_j as three bf16 parts
-// (24 bits), so its products are those of fp32; L is summed in 64 bits, and every exponent
-// is a difference of L's taken before it is rounded.
+// (24 bits), so its products are those of fp32.  L is summed in 64 bits and differences of it are taken
+// before they are rounded to floats: over a block of 32 tokens, to a chunk's end, and between blocks.  The
+// exponents of P and of Q S^T's scale are the sum or difference of two such floats, each off by at most 2^-24 of
+// itself: 2^-11 together where a block has 31 zero decays, 2^-15 with one or two, and P is rounded to bf16 (2^-9).
 //
 // Warp roles (16 warps, bounded mbarrier waits): a producer (TMA: Q, V, K tiles of 32 KB into a
 // ring of five), two MMA issuers (of P and O, and of the state's update, so that neither waits for
@@ -30,8 +32,9 @@
 // memory as the A operand, 16 tokens at a time in two alternating buffers for each half, then add the product
 // to their registers and write the bf16 copy of S for the next chunk's Q S^T.
 //
-// 8192 tokens of 32 heads of 128 x 128 (205 MB): 92 us (4802 by the walk on the CUDA cores); twelve
-// packed sequences of 4956 tokens in all, 80 heads of 64 x 128: 84 us.  A chunk takes 5750
+// 8192 tokens of 32 heads of 128 x 128 (205 MB): 91 us in a loop of one call, 102 among calls on changing
+// inputs (4802 by the walk on the CUDA cores); twelve
+// packed sequences of 4956 tokens in all, 80 heads of 64 x 128: 84 us either way.  A chunk takes 5750
 // cycles, against 3100 of the tensor cores and 3800 of shared memory (operands, copies, rows of O):
 // the loop that bounds it runs over the warps of P and O (O's rows read and sent out 1500, P 2000 for
 // the first tokens and 2800 for the last, P V 800, Q K^T of the next chunk between).

@@ -11,16 +11,17 @@
 // into equal contiguous shares, one per CTA (two CTAs per SM), so ragged lengths, one
 // long sequence and many short ones all load the SMs evenly.  A producer warp fetches the
 // page ids one block ahead and issues one TMA box per run of rows inside a page (at most
-// eight per block, each lane its own) into a ring of stages; four warps take 16 positions
-// of the block each, with their own running maximum, sum and output (one pass, online
+// sixteen per block, each lane its own) into a ring of stages; four warps take a quarter of
+// the block each (16 positions, 32 with 8-bit pages), with their own running maximum, sum and output (one pass, online
 // softmax), and are joined in shared memory where the share leaves a row of blocks.  A row
 // of blocks that lies in one share is finished there; the pieces of the others go to the
 // workspace and a second launch joins them by the log-sum-exp rule.
 //
-// The products run on the warp-level matrix instruction with the query heads as its 16
-// rows: the operands arrive by ldmatrix straight from the swizzled tile and the scores
-// stay in registers as the next product's operand; a 128-row tcgen05 tile would be at
-// most one eighth full and adds a round trip through tensor memory for each block.
+// The products run on the warp-level matrix instruction.  K Q^T: 16 keys are its rows and eight
+// query heads its columns.  V^T P: 16 value columns are its rows, the heads its columns again.  K and V
+// arrive by ldmatrix straight from the swizzled tile; the probabilities stay in registers and are
+// turned into the second product's operand by a transposing move.  A 128-row tcgen05 tile of query heads
+// would be at most one eighth full and adds a round trip through tensor memory for each block.
 // 8-bit pages: keys and values become fp16 exactly (every e4m3 is one).  A query row is
 // scaled to [-2^15, 2^15] by a power of two so that it is fp16 as well, exactly down to 2^-31 of
 // the row's largest element (below, to 2^-40 of it; scaled to [-1, 1], elements below 2^-16 lost bits that
@@ -30,12 +31,13 @@
 // 2^15, none overflows whatever the scales, and a weight has fp16's eleven bits down to 2^-29 of the largest
 // and is gone below 2^-40.  (With a largest weight of 1 those were 2^-14 and 2^-25: a key that takes nearly all
 // of the softmax with a value near zero left nothing of the others.)  (Values widened to bf16 with the scale on a bf16
-// probability: 120 us; so and with page positions followed without divisions 93; with the keys as
-// the instruction's rows for up to eight heads, below, 60.)
+// probability: 120 us; so and with page positions followed without divisions 93; with the keys
+// and not 16 query heads as the instruction's rows 60.)
 //
-// Measured: one sequence of 131065 tokens, bf16, 32 heads over 8 (537 MB): 94 us a call, 82 of
-// them this kernel's (6.5 TB/s, a copy's rate) and the rest the join's; 64 sequences of up to
-// 4096 tokens, e4m3 (272 MB): 67 us, bound by the conversion's instructions and the join.
+// Measured, calls one behind the other on changing inputs: one sequence of 131065 tokens, bf16, 32 heads over 8
+// (537 MB): 94 us a call, 82 of them this kernel's (6.5 TB/s, a copy's rate) and the rest the join's; 64 sequences of
+// up to 4096 tokens, e4m3 (272 MB): 68 us, with 53 % of DRAM and 45 % of the issue slots in use: the chain of a
+// block's steps in each warp (conversion, scores, maxima, exponentials, conversion, values) and the join.
 #include <cuda.h>
 
 #include <mutex>

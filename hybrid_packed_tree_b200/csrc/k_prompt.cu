@@ -35,6 +35,8 @@
 // The reference maximum moves only when a block exceeds it by 2^8 (output and sum are then
 // rescaled together): P stays below 256 and O / l is the same softmax.  Scores and sums are
 // fp32; P is rounded to bf16, the type of the values it multiplies.
+// Times above are of one call in loops too short for the card's power cap; under it, among calls on changing
+// inputs, 8192 tokens take 485 us and a packed batch of 5604 tokens 70 us.  The stores below were compared so.
 // The mask is applied before any maximum or exponential.  Value rows behind the end of the
 // sequence (another sequence's) are zeroed in shared memory before use: 0 x NaN would reach
 // the sum otherwise.

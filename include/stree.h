@@ -83,7 +83,7 @@ typedef enum {
     STREE_ERR_BAD_PATH = 4,     /* device-detected: accepted path is not a root->node chain */
     STREE_ERR_MISALIGNED = 5,   /* a tensor pointer is not 16-byte aligned */
     STREE_ERR_CUDA = 6,         /* a CUDA runtime call failed (launch, allocation) */
-    STREE_ERR_TIMEOUT = 7,      /* a bounded wait inside the tensor-core kernel gave up (about 1 s) */
+    STREE_ERR_TIMEOUT = 7,      /* a bounded wait inside a kernel gave up (about 1 s) */
     STREE_ERR_NO_TREE = 8,      /* scan with parent = NULL before any tree was built, or
                                    commit before any scan, or a size mismatch with them */
     STREE_ERR_BAD_SEQ = 9,      /* device-detected: packed offsets not ascending in [0, total] */
@@ -418,7 +418,9 @@ stree_status stree_tree_attention_workspace_size(int n_nodes, int batch, int ctx
  *   has rows cu_seqlens[b] .. cu_seqlens[b+1] - 1 (device int32 [batch + 1], ascending
  *   in [0, total]; equal entries are an empty sequence).  Rows behind the last sequence
  *   are neither read into a result nor written.  A sequence whose pair of offsets is not
- *   ascending in [0, total] counts as empty and latches STREE_ERR_BAD_SEQ.
+ *   ascending in [0, total] counts as empty and latches STREE_ERR_BAD_SEQ; where others
+ *   overlap beside it, a row that several claim holds the result of one of them, and
+ *   stree_prompt_attention may leave rows of other sequences unwritten.
  *
  *   Paged cache: k_pages, v_pages [n_pages, heads_kv, page_size, 128]; position j of
  *   sequence b is row j % page_size of page page_table[b][j / page_size] (device int32
@@ -431,7 +433,8 @@ stree_status stree_tree_attention_workspace_size(int n_nodes, int batch, int ctx
  *   STREE_ERR_BAD_PAGE; no memory outside the pages is touched.
  *
  *   err_out: device int32[4] error word of this call (cleared by the call), or NULL to
- *   discard device-detected errors.  No call allocates; every call runs on `stream`, on
+ *   discard device-detected errors.  After STREE_ERR_TIMEOUT (stree_set_wait_hook) the
+ *   outputs are incomplete, a state updated in place among them.  No call allocates; every call runs on `stream`, on
  *   the current device, and may be captured in a CUDA graph.  A workspace belongs to the
  *   caller, holds nothing between calls, and may be shared by calls (captured ones
  *   too) that are ordered.  Inputs must be finite; what lies behind a sequence's end
@@ -460,7 +463,7 @@ stree_status stree_tree_attention_workspace_size(int n_nodes, int batch, int ctx
  * Shapes: dk and dv multiples of 8 up to 256, heads_v a multiple of heads_k.  fp32 inputs
  * and shapes other than those below run on CUDA cores in fp32.  bf16 with dk = 128 and dv =
  * 128, or dv = 64 with an even number of value heads per key head, runs in chunks of 128
- * tokens on the tensor cores: the pair weights and the state that a chunk's queries
+ * tokens on the tensor cores: the pair weights (the skip among them) and the state that a chunk's queries
  * read are rounded to bf16 (they only enter o, itself bf16); the state itself is
  * accumulated in fp32 from fp32 products.
  */
